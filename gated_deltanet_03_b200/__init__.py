@@ -9,6 +9,8 @@ Functions keep the C names:
   gdn_decode_commit, gdn_gated_rmsnorm_silu,
   gdn_gated_rmsnorm_silu_nvfp4, nvfp4_quantize_act, nvfp4_dequantize_act, nvfp4_gemm,
   nvfp4_gemm_colscale, gdn_short_conv1d_silu, gdn_short_conv1d_silu_decode,
+  fp8_quantize_act, fp8_quantize_weight, fp8_gemm, gdn_gated_rmsnorm_silu_fp8,
+  gdn_decode_step_pooled, gdn_decode_step_pooled_gated_fp8, gdn_short_conv1d_silu_decode_pooled,
   gdn_prefill_workspace_bytes, gdn_get_device_status.
 """
 from __future__ import annotations
@@ -30,7 +32,10 @@ ABI_SYMBOLS = (
     "gdn_decode_step_gated_nvfp4",
     "gdn_decode_verify", "gdn_decode_commit",
     "gdn_gated_rmsnorm_silu", "gdn_gated_rmsnorm_silu_nvfp4", "nvfp4_quantize_act", "nvfp4_dequantize_act",
-    "nvfp4_gemm", "nvfp4_gemm_colscale", "nvfp4_fused_col_alpha", "q4k_gemm", "gdn_short_conv1d_silu", "gdn_short_conv1d_silu_decode",
+    "nvfp4_gemm", "nvfp4_gemm_colscale", "nvfp4_fused_col_alpha", "q4k_gemm",
+    "fp8_quantize_act", "fp8_quantize_weight", "gdn_gated_rmsnorm_silu_fp8", "fp8_gemm",
+    "gdn_decode_step_pooled", "gdn_decode_step_pooled_gated_fp8",
+    "gdn_short_conv1d_silu", "gdn_short_conv1d_silu_decode", "gdn_short_conv1d_silu_decode_pooled",
     "gdn_prefill_chunked_static_ws", "gdn_get_device_status", "gdn_debug_set_wait", "gdn_status_string",
     "gdn_version",
 )
@@ -74,6 +79,15 @@ def _load() -> ctypes.CDLL:
     lib.gdn_short_conv1d_silu_decode.argtypes = [P, i64, P, i32, i32, i32, P, P, P, i32, P]
     lib.gdn_prefill_chunked_static_ws.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, f32,
                                                   i32, i32, P, P, P, i32, P]
+    lib.fp8_quantize_act.argtypes = [P, i64, i32, i32, i32, P, P, P]
+    lib.fp8_quantize_weight.argtypes = [P, i64, i32, i32, i32, P, P, P]
+    lib.gdn_gated_rmsnorm_silu_fp8.argtypes = [P, P, P, f32, i32, i32, i32, i32, P, P, P]
+    lib.fp8_gemm.argtypes = [P, P, P, P, i32, i32, i32, i32, P, P]
+    lib.gdn_decode_step_pooled.argtypes = [P, P, P, P, P, i64, i32, P, P, i32, i32, i32, i32, i32, f32, i32, i32,
+                                           P, i32, P, P, i32, P]
+    lib.gdn_decode_step_pooled_gated_fp8.argtypes = [P, P, P, P, P, i64, i32, P, P, i32, i32, i32, i32, i32, f32, i32,
+                                                     i32, P, i32, P, P, i64, P, f32, P, P, P, P]
+    lib.gdn_short_conv1d_silu_decode_pooled.argtypes = [P, i64, P, i32, i32, i32, P, i32, P, P, P, i32, P]
     lib.gdn_get_device_status.argtypes = [P]
     lib.gdn_debug_set_wait.argtypes = [ctypes.c_uint64, ctypes.c_uint32]
     lib.gdn_status_string.argtypes = [i32]
@@ -84,6 +98,8 @@ def _load() -> ctypes.CDLL:
                  "gdn_decode_commit", "gdn_gated_rmsnorm_silu",
                  "gdn_gated_rmsnorm_silu_nvfp4", "nvfp4_quantize_act", "nvfp4_dequantize_act", "nvfp4_gemm",
                  "nvfp4_gemm_colscale", "nvfp4_fused_col_alpha", "q4k_gemm",
+                 "fp8_quantize_act", "fp8_quantize_weight", "gdn_gated_rmsnorm_silu_fp8", "fp8_gemm",
+                 "gdn_decode_step_pooled", "gdn_decode_step_pooled_gated_fp8", "gdn_short_conv1d_silu_decode_pooled",
                  "gdn_short_conv1d_silu", "gdn_short_conv1d_silu_decode", "gdn_get_device_status", "gdn_debug_set_wait"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -498,6 +514,186 @@ def gdn_short_conv1d_silu_decode(x, weight, conv_state, parts=None, y=None, stre
                                           len(arr), _stream(stream))
     _check("gdn_short_conv1d_silu_decode", st)
     return views[0] if parts is None else views
+
+
+# ---------------------------------------------------- FP8 and pooled decode ----
+# These calls run on the device of their tensors, whichever device is current, and outputs that they
+# allocate belong to the stream that writes them.
+
+_F8, _BF = (torch.float8_e4m3fn,), (torch.bfloat16,)
+
+
+def _launch(name, device, stream, *args):
+    """The library call `name` on `stream` (default: the device's current stream)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError("stream is on %s, the call's tensors on %s" % (stream.device, device))
+    if device.index == torch.cuda.current_device():
+        st = getattr(LIB, name)(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(LIB, name)(*args, stream.cuda_stream)
+    if st != GDN_OK:
+        raise GdnError(name, st)
+
+
+def _new(shape, dtype, device, stream, like=torch.empty):
+    if stream is None:
+        return like(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return like(shape, dtype=dtype, device=device)
+
+
+def _rows2d(name, t):
+    """Row stride of a 2-D tensor whose rows may be strided (a column slice of a wider matrix)."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be 2-D with unit column stride" % name)
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _fp8_quantize(name, x, xq, xs, srows, stream):
+    ldx = _rows2d("x", x)
+    M, K = x.shape
+    kb = (K + 127) // 128
+    _args(x.device, x=(x, _IO, None), xq=(xq, _F8, M * K), xs=(xs, _F32, srows * kb))
+    _contig(xq, xs)
+    if xq is None:
+        xq = _new((M, K), torch.float8_e4m3fn, x.device, stream)
+    if xs is None:
+        xs = _new((srows, kb), torch.float32, x.device, stream)
+    _launch(name, x.device, stream, x.data_ptr(), ldx, _dt(x), M, K, xq.data_ptr(), xs.data_ptr())
+    return xq, xs
+
+
+def fp8_quantize_act(x, xq=None, xs=None, stream=None):
+    """x [M, K] bf16/fp32 (rows may be strided) -> (xq [M, K] float8_e4m3fn, xs [M, ceil(K/128)] fp32),
+    one scale per 128 values of a row. K % 16 == 0."""
+    return _fp8_quantize("fp8_quantize_act", x, xq, xs, x.shape[0], stream)
+
+
+def fp8_quantize_weight(w, wq=None, ws=None, stream=None):
+    """w [N, K] bf16/fp32 (rows may be strided) -> (wq [N, K] float8_e4m3fn, ws [ceil(N/128), ceil(K/128)] fp32),
+    one scale per 128 x 128 block. K % 16 == 0."""
+    return _fp8_quantize("fp8_quantize_weight", w, wq, ws, (w.shape[0] + 127) // 128, stream)
+
+
+def fp8_gemm(aq, as_, bq, bs, out_dtype=torch.bfloat16, y=None, stream=None):
+    """(aq [M, K], as [M, ceil(K/128)]) x (bq [N, K], bs [ceil(N/128), ceil(K/128)])^T -> y [M, N]."""
+    M, K = aq.shape
+    N = bq.shape[0]
+    kb = (K + 127) // 128
+    _args(aq.device, aq=(aq, _F8, None), as_=(as_, _F32, M * kb), bq=(bq, _F8, N * K),
+          bs=(bs, _F32, (N + 127) // 128 * kb), y=(y, _IO, M * N))
+    _contig(aq, as_, bq, bs, y)
+    if bq.shape[1] != K:
+        raise ValueError("bq has %d columns, aq %d" % (bq.shape[1], K))
+    if y is None:
+        y = _new((M, N), out_dtype, aq.device, stream)
+    _launch("fp8_gemm", aq.device, stream, aq.data_ptr(), as_.data_ptr(), bq.data_ptr(), bs.data_ptr(), M, N, K, _dt(y),
+            y.data_ptr())
+    return y
+
+
+def gdn_gated_rmsnorm_silu_fp8(o, z, weight, eps: float = 1e-6, xq=None, xs=None, stream=None):
+    """o, z [M, Hv, D] -> (xq [M, Hv * D] float8_e4m3fn, xs [M, ceil(Hv * D / 128)] fp32)."""
+    M, Hv, D = o.shape
+    kb = (Hv * D + 127) // 128
+    _args(o.device, o=(o, _IO, None), z=(z, (o.dtype,), M * Hv * D), weight=(weight, _F32, D),
+          xq=(xq, _F8, M * Hv * D), xs=(xs, _F32, M * kb))
+    _contig(o, z, weight, xq, xs)
+    if xq is None:
+        xq = _new((M, Hv * D), torch.float8_e4m3fn, o.device, stream)
+    if xs is None:
+        xs = _new((M, kb), torch.float32, o.device, stream)
+    _launch("gdn_gated_rmsnorm_silu_fp8", o.device, stream, o.data_ptr(), z.data_ptr(), weight.data_ptr(), eps, M, Hv, D,
+            _dt(o), xq.data_ptr(), xs.data_ptr())
+    return xq, xs
+
+
+def _pooled_args(q, k, v, a, b, A_log, dt_bias, state_pool, slots, **more):
+    """Checks shared by the pooled decode calls; returns (B, Hk, Hv, D, gate row stride)."""
+    if any(t is None for t in (a, b, state_pool, slots)):
+        raise ValueError("a, b, state_pool and slots are required")
+    B, Hk, D = q.shape
+    Hv = v.shape[1]
+    if state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (Hv, D, D):
+        raise ValueError("state_pool must be [num_slots, %d, %d, %d]" % (Hv, D, D))
+    if a.shape != (B, Hv) or b.shape != (B, Hv) or v.shape != (B, Hv, D) or k.shape != q.shape:
+        raise ValueError("a, b must be [%d, %d], v [%d, %d, %d], k as q" % (B, Hv, B, Hv, D))
+    _args(q.device, q=(q, _BF, None), k=(k, _BF, None), v=(v, _BF, None), a=(a, _IO, None), b=(b, (a.dtype,), None),
+          A_log=(A_log, _F32, Hv), dt_bias=(dt_bias, _F32, Hv), state_pool=(state_pool, _F32, None),
+          slots=(slots, _I32, B), **more)
+    _contig(q, k, v, A_log, dt_bias, state_pool, slots)
+    ldg = _rows2d("a", a)
+    if _rows2d("b", b) != ldg:
+        raise ValueError("a and b must have the same row stride")
+    return B, Hk, Hv, D, ldg
+
+
+def gdn_decode_step_pooled(q, k, v, a, b, A_log, dt_bias, state_pool, slots, scale: float = 1.0,
+                           qk_l2norm: bool = True, out_dtype=None, o=None, stream=None):
+    """gdn_decode_step on states in a pool: row i uses slot slots[i] (device int32 [B]) of state_pool
+    [num_slots, Hv, 128, 128] fp32, in place; a negative slot marks a padded row, whose state and output
+    stay as they are (a new output is zero there). a, b [B, Hv] bf16 or fp32, rows may be strided. Returns o."""
+    B, Hk, Hv, D, ldg = _pooled_args(q, k, v, a, b, A_log, dt_bias, state_pool, slots, o=(o, _IO, v.numel()))
+    _contig(o)
+    if o is None:
+        o = _new((B, Hv, D), out_dtype or q.dtype, q.device, stream, torch.zeros)
+    _launch("gdn_decode_step_pooled", q.device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(),
+            ldg, _dt(a), A_log.data_ptr(), dt_bias.data_ptr(), B, Hk, Hv, D, D, scale, int(bool(qk_l2norm)), GDN_BF16,
+            state_pool.data_ptr(), state_pool.shape[0], slots.data_ptr(), o.data_ptr(), _dt(o))
+    return o
+
+
+def gdn_decode_step_pooled_gated_fp8(q, k, v, a, b, A_log, dt_bias, state_pool, slots, z, norm_weight,
+                                     scale: float = 1.0, qk_l2norm: bool = True, eps: float = 1e-6, xq=None, xs=None,
+                                     o=None, stream=None):
+    """gdn_decode_step_pooled with the gated RMSNorm and its FP8 encode fused: z [B, Hv, 128] bf16 (rows may
+    be strided), norm_weight [128] fp32. Returns (xq [B, Hv*128] float8_e4m3fn, xs [B, Hv] fp32, o or None);
+    o (bf16) is written only when given. New outputs are zero in padded rows."""
+    if z is None or norm_weight is None:
+        raise ValueError("z and norm_weight are required")
+    n = v.numel()
+    B, Hk, Hv, D, ldg = _pooled_args(q, k, v, a, b, A_log, dt_bias, state_pool, slots, z=(z, _BF, None),
+                                     norm_weight=(norm_weight, _F32, 128), xq=(xq, _F8, n), xs=(xs, _F32, n // 128),
+                                     o=(o, _BF, n))
+    _contig(norm_weight, xq, xs, o)
+    if z.shape != v.shape or (z.stride(2), z.stride(1)) != (1, D) and (Hv > 1 or z.stride(2) != 1):
+        raise ValueError("z must be [%d, %d, %d] with contiguous heads" % (B, Hv, D))
+    ldz = z.stride(0) if B > 1 else Hv * D
+    if xq is None:
+        xq = _new((B, Hv * D), torch.float8_e4m3fn, q.device, stream, torch.zeros)
+    if xs is None:
+        xs = _new((B, Hv), torch.float32, q.device, stream, torch.zeros)
+    _launch("gdn_decode_step_pooled_gated_fp8", q.device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(),
+            b.data_ptr(), ldg, _dt(a), A_log.data_ptr(), dt_bias.data_ptr(), B, Hk, Hv, D, D, scale, int(bool(qk_l2norm)),
+            GDN_BF16, state_pool.data_ptr(), state_pool.shape[0], slots.data_ptr(), z.data_ptr(), ldz,
+            norm_weight.data_ptr(), eps, xq.data_ptr(), xs.data_ptr(), None if o is None else o.data_ptr())
+    return xq, xs, o
+
+
+def gdn_short_conv1d_silu_decode_pooled(x, weight, conv_pool, slots, parts=None, y=None, stream=None):
+    """gdn_short_conv1d_silu_decode on a pool: row i shifts slot slots[i] (device int32 [B], negative: a
+    padded row, left as it is; a new y is zero there) of conv_pool bf16 [num_slots, K - 1, C] in place."""
+    B, C, ldx = _conv_rows(x)
+    K = weight.shape[1]
+    if conv_pool is None or slots is None:
+        raise ValueError("conv_pool and slots are required")
+    if conv_pool.dim() != 3 or tuple(conv_pool.shape[1:]) != (K - 1, C) or weight.shape[0] != C:
+        raise ValueError("conv_pool must be [num_slots, %d, %d] and weight [%d, K]" % (K - 1, C, C))
+    _args(x.device, x=x, weight=(weight, _F32, None), conv_pool=(conv_pool, _BF, None), slots=(slots, _I32, B),
+          y=(y, _BF, B * C))
+    _contig(weight, conv_pool, slots, y)
+    if y is None:
+        y = _new((B, C) if parts is None else (B * C,), torch.bfloat16, x.device, stream, torch.zeros)
+    widths = [C] if parts is None else [int(p) for p in parts]
+    _launch("gdn_short_conv1d_silu_decode_pooled", x.device, stream, x.data_ptr(), ldx, weight.data_ptr(), B, C, K,
+            conv_pool.data_ptr(), conv_pool.shape[0], slots.data_ptr(), y.data_ptr(),
+            (ctypes.c_int32 * len(widths))(*widths), len(widths))
+    if parts is None:
+        return y.view(-1)[:B * C].view(B, C)
+    return _conv_planes(parts, B, C, y, x.device)[2]
 
 
 INJECT_SKIP_PREP_LOADS = 1

@@ -320,6 +320,96 @@ gdn_status q4k_gemm(const void *a, const uint8_t *w, int32_t M, int32_t N, int32
     return launched(gdn::launch_q4k_gemm(g, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static gdn_status fp8_quantize(const void *x, int64_t ldx, gdn_dtype in_dtype, bool weight, int32_t rows, int32_t K,
+                               uint8_t *xq, float *xs, gdn_stream_t stream) {
+    if (rows < 0 || K < 0 || ldx < K || !dtype_ok(in_dtype)) return GDN_ERR_INVALID_ARG;
+    if (K % 16 != 0) return GDN_ERR_UNSUPPORTED;
+    if (rows == 0 || K == 0) return GDN_OK;
+    if ((int64_t)rows * ((K + 127) / 128) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (!x || !xq || !xs || !aligned16(x) || !aligned16(xq) || ldx % (in_dtype == GDN_BF16 ? 8 : 4) != 0)
+        return GDN_ERR_INVALID_ARG;
+    gdn::Fp8QuantArgs a{x, ldx, in_dtype == GDN_BF16, weight, rows, K, xq, xs};
+    return launched(gdn::launch_fp8_quantize(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status fp8_quantize_act(const void *x, int64_t ldx, gdn_dtype in_dtype, int32_t M, int32_t K, uint8_t *xq,
+                            float *xs, gdn_stream_t stream) {
+    return fp8_quantize(x, ldx, in_dtype, false, M, K, xq, xs, stream);
+}
+
+gdn_status fp8_quantize_weight(const void *w, int64_t ldw, gdn_dtype in_dtype, int32_t N, int32_t K, uint8_t *wq,
+                               float *ws, gdn_stream_t stream) {
+    return fp8_quantize(w, ldw, in_dtype, true, N, K, wq, ws, stream);
+}
+
+gdn_status gdn_gated_rmsnorm_silu_fp8(const void *o, const void *z, const float *weight, float eps, int32_t M,
+                                      int32_t Hv, int32_t Dv, gdn_dtype in_dtype, uint8_t *xq, float *xs,
+                                      gdn_stream_t stream) {
+    gdn_status s = tail_check(o, z, weight, eps, M, Hv, Dv, in_dtype);
+    if (s != GDN_OK) return s;
+    const int64_t K = (int64_t)Hv * Dv;
+    if (K > INT32_MAX - 127 || M * ((K + 127) / 128) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (M == 0) return GDN_OK;
+    if (!xq || !xs || !aligned16(xq)) return GDN_ERR_INVALID_ARG;
+    gdn::Fp8TailArgs t{o, z, weight, eps, M, Hv, Dv, in_dtype == GDN_BF16, xq, xs};
+    return launched(gdn::launch_gated_rmsnorm_fp8(t, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status fp8_gemm(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs, int32_t M, int32_t N,
+                    int32_t K, gdn_dtype out_dtype, void *y, gdn_stream_t stream) {
+    if (M < 0 || N < 0 || K < 0 || !dtype_ok(out_dtype)) return GDN_ERR_INVALID_ARG;
+    if (K % 16 != 0 || N % 16 != 0 || M > 128 * 65535) return GDN_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return GDN_OK;
+    if (K == 0) return GDN_ERR_UNSUPPORTED;
+    if (!aq || !as || !bq || !bs || !y) return GDN_ERR_INVALID_ARG;
+    if (!aligned16(aq) || !aligned16(bq) || !aligned16(y)) return GDN_ERR_INVALID_ARG;
+    gdn::Fp8GemmArgs g{aq, as, bq, bs, M, N, K, out_dtype == GDN_BF16, y, status_ptr()};
+    return launched(gdn::launch_fp8_gemm(g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static gdn_status pooled_decode(gdn::PooledDecodeArgs &d, int32_t Dk, int32_t Dv, gdn_dtype gate_dtype,
+                                gdn_dtype in_dtype, gdn_dtype out_dtype, gdn_stream_t stream) {
+    if (d.B < 0 || d.Hk < 1 || d.Hv < 1 || d.Hv % d.Hk != 0 || d.num_slots < 0 || d.ldg < d.Hv)
+        return GDN_ERR_INVALID_ARG;
+    if (!dtype_ok(gate_dtype) || !dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return GDN_ERR_INVALID_ARG;
+    if (Dk != 128 || Dv != 128 || in_dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+    if ((int64_t)d.B * d.Hv > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (d.B == 0) return GDN_OK;
+    if (!d.q || !d.k || !d.v || !d.a || !d.b || !d.A_log || !d.dt_bias || !d.slots || (!d.pool && d.num_slots > 0))
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned16(d.q) || !aligned16(d.k) || !aligned16(d.v) || !aligned16(d.pool) || (d.o && !aligned16(d.o)))
+        return GDN_ERR_INVALID_ARG;
+    d.gate_bf16 = gate_dtype == GDN_BF16;
+    d.out_bf16 = out_dtype == GDN_BF16;
+    d.status = status_ptr();
+    return launched(gdn::launch_decode_pooled(d, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_decode_step_pooled(const void *q, const void *k, const void *v, const void *a, const void *b,
+                                  int64_t ldg, gdn_dtype gate_dtype, const float *A_log, const float *dt_bias,
+                                  int32_t B, int32_t Hk, int32_t Hv, int32_t Dk, int32_t Dv, float scale,
+                                  int32_t qk_l2norm, gdn_dtype in_dtype, float *state_pool, int32_t num_slots,
+                                  const int32_t *slots, void *o, gdn_dtype out_dtype, gdn_stream_t stream) {
+    if (B > 0 && !o) return GDN_ERR_INVALID_ARG;
+    gdn::PooledDecodeArgs d{q, k, v, a, b, ldg, false, A_log, dt_bias, B, Hk, Hv, scale, qk_l2norm, state_pool,
+                            num_slots, slots, o};
+    return pooled_decode(d, Dk, Dv, gate_dtype, in_dtype, out_dtype, stream);
+}
+
+gdn_status gdn_decode_step_pooled_gated_fp8(const void *q, const void *k, const void *v, const void *a, const void *b,
+                                            int64_t ldg, gdn_dtype gate_dtype, const float *A_log,
+                                            const float *dt_bias, int32_t B, int32_t Hk, int32_t Hv, int32_t Dk,
+                                            int32_t Dv, float scale, int32_t qk_l2norm, gdn_dtype in_dtype,
+                                            float *state_pool, int32_t num_slots, const int32_t *slots,
+                                            const void *z, int64_t ldz, const float *norm_weight, float eps,
+                                            uint8_t *xq, float *xs, void *o, gdn_stream_t stream) {
+    if (!(eps >= 0.0f) || ldz % 8 != 0 || ldz < (int64_t)Hv * Dv) return GDN_ERR_INVALID_ARG;
+    if (B > 0 && (!z || !norm_weight || !xq || !xs || !aligned16(z) || !aligned16(xq))) return GDN_ERR_INVALID_ARG;
+    gdn::PooledDecodeArgs d{q, k, v, a, b, ldg, false, A_log, dt_bias, B, Hk, Hv, scale, qk_l2norm, state_pool,
+                            num_slots, slots, o, true, z, ldz, norm_weight, eps, xq, xs};
+    return pooled_decode(d, Dk, Dv, gate_dtype, in_dtype, GDN_BF16, stream);
+}
+
 gdn_status nvfp4_fused_col_alpha(const int32_t *widths, const float *module_scales, int32_t n_modules,
                                  float act_scale, float *col_alpha, gdn_stream_t stream) {
     if (!widths || !module_scales || !col_alpha || n_modules < 1 || n_modules > gdn::kMaxModules)
@@ -407,9 +497,9 @@ gdn_status gdn_short_conv1d_silu(const void *x, int64_t ldx, const float *weight
     return launched(gdn::launch_short_conv(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-gdn_status gdn_short_conv1d_silu_decode(const void *x, int64_t ldx, const float *weight, int32_t B, int32_t C,
-                                        int32_t K, void *conv_state, void *y, const int32_t *part_widths,
-                                        int32_t n_parts, gdn_stream_t stream) {
+static gdn_status conv_decode(const void *x, int64_t ldx, const float *weight, int32_t B, int32_t C, int32_t K,
+                              void *conv_state, int32_t states, const int32_t *slots, void *y,
+                              const int32_t *part_widths, int32_t n_parts, gdn_stream_t stream) {
     if (B < 0 || K < 1 || C < 0) return GDN_ERR_INVALID_ARG;
     if (K > 4) return GDN_ERR_UNSUPPORTED;
     if (B == 0 || C == 0) return GDN_OK;
@@ -417,10 +507,11 @@ gdn_status gdn_short_conv1d_silu_decode(const void *x, int64_t ldx, const float 
     gdn::ConvArgs a{};
     if (!conv_planes(part_widths, n_parts, C, a)) return GDN_ERR_INVALID_ARG;
     if (!conv_common_ok(x, ldx, weight, C, K, y)) return GDN_ERR_INVALID_ARG;
-    const size_t state_bytes = (size_t)B * (K - 1) * C * 2;
-    if (K > 1 && (!conv_state || !aligned16(conv_state))) return GDN_ERR_INVALID_ARG;
-    if (K > 1 && (overlaps(conv_state, state_bytes, x, (size_t)B * ldx * 2) ||
-                  overlaps(conv_state, state_bytes, y, (size_t)B * C * 2)))
+    const size_t state_bytes = (size_t)states * (K - 1) * C * 2;
+    if (state_bytes && (!conv_state || !aligned16(conv_state))) return GDN_ERR_INVALID_ARG;
+    // x may be a column block: its last row ends C elements after that row's start
+    if (overlaps(conv_state, state_bytes, x, ((size_t)(B - 1) * ldx + C) * 2) ||
+        overlaps(conv_state, state_bytes, y, (size_t)B * C * 2))
         return GDN_ERR_INVALID_ARG;
     a.x = x;
     a.ldx = ldx;
@@ -432,7 +523,26 @@ gdn_status gdn_short_conv1d_silu_decode(const void *x, int64_t ldx, const float 
     a.final_state = conv_state;
     a.y = y;
     a.decode = true;
+    a.slots = slots;
+    a.num_slots = states;
+    a.status = slots ? status_ptr() : nullptr;
     return launched(gdn::launch_short_conv(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_short_conv1d_silu_decode(const void *x, int64_t ldx, const float *weight, int32_t B, int32_t C,
+                                        int32_t K, void *conv_state, void *y, const int32_t *part_widths,
+                                        int32_t n_parts, gdn_stream_t stream) {
+    return conv_decode(x, ldx, weight, B, C, K, conv_state, B, nullptr, y, part_widths, n_parts, stream);
+}
+
+gdn_status gdn_short_conv1d_silu_decode_pooled(const void *x, int64_t ldx, const float *weight, int32_t B, int32_t C,
+                                               int32_t K, void *conv_pool, int32_t num_slots, const int32_t *slots,
+                                               void *y, const int32_t *part_widths, int32_t n_parts,
+                                               gdn_stream_t stream) {
+    if (num_slots < 0) return GDN_ERR_INVALID_ARG;
+    if (B > 4 * 65535) return GDN_ERR_UNSUPPORTED;
+    if (B > 0 && C > 0 && !slots) return GDN_ERR_INVALID_ARG;
+    return conv_decode(x, ldx, weight, B, C, K, conv_pool, num_slots, slots, y, part_widths, n_parts, stream);
 }
 
 }  // extern "C"

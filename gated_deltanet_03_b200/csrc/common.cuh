@@ -184,6 +184,25 @@ GDN_DEV float amax8(const float (&x)[8]) {
     return m;
 }
 
+// ----------------------------------------------------------------- FP8 convert ----
+
+// Scale of one FP8 block from its largest magnitude, s = max(amax / 448, 2^-126), and the factor
+// r = 1 / s that maps values to codes. The floor keeps r finite and the codes of an all-zero block
+// zero; an infinite amax gives s = inf and r = 0 (the infinities' codes are NaN, 0 * inf).
+GDN_DEV float fp8_block_scale(float amax, float &r) {
+    const float s = fmaxf(__fdiv_rn(amax, 448.0f), 0x1p-126f);
+    r = __frcp_rn(s);
+    return s;
+}
+
+// Four E4M3 codes of x * r (nearest, ties to even, saturating at 448, NaN kept), first in the low byte.
+GDN_DEV uint32_t fp8_pack4(float x0, float x1, float x2, float x3, float r) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fmul_rn(x1, r)), "f"(__fmul_rn(x0, r)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fmul_rn(x3, r)), "f"(__fmul_rn(x2, r)));
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
 // -------------------------------------------------------------- device status ----
 
 // The library's device control block: the status word that bounded waits report into, the

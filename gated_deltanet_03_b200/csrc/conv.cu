@@ -270,10 +270,14 @@ short_conv_state_kernel(const void *__restrict__ x, int64_t ldx, const int32_t *
 
 // One token per sequence, kDecRows sequences per thread: y from the carried state and x, then
 // the state shifted by one. The inputs are requested before the weights.
-template <int K>
+// POOLED: sequence b's state is slot slots[b] of a pool. A row with a negative slot is passed over (its y stays
+// as it is), and so is one whose slot is not below num_slots or is named by an earlier row, with
+// GDN_ERR_INVALID_ARG in the status word; the look through the earlier rows runs beside the state loads.
+template <int K, bool POOLED>
 __global__ void __launch_bounds__(kConvThreads)
 short_conv_decode_kernel(const void *__restrict__ x, int64_t ldx, const float *__restrict__ w, int32_t B,
-                         int32_t C, void *state, void *__restrict__ y, Planes pl) {
+                         int32_t C, void *state, void *__restrict__ y, Planes pl, const int32_t *__restrict__ slots,
+                         int32_t num_slots, int *status) {
     __shared__ float4 wsm[kConvThreads * 2 * K];
     pdl_launch_dependents();
     pdl_wait();
@@ -282,13 +286,32 @@ short_conv_decode_kernel(const void *__restrict__ x, int64_t ldx, const float *_
     const int b0 = blockIdx.y * kDecRows;
     const bool active = c0 < C;
     uint4 xr[kDecRows], sr[kDecRows][K > 1 ? K - 1 : 1];
+    int32_t at[kDecRows];
+#pragma unroll
+    for (int r = 0; r < kDecRows; ++r) at[r] = b0 + r < B ? (POOLED ? slots[b0 + r] : b0 + r) : -1;
 #pragma unroll
     for (int r = 0; r < kDecRows; ++r)
-        if (active && b0 + r < B) {
+        if (active && at[r] >= 0 && (!POOLED || at[r] < num_slots)) {
             xr[r] = ld16(x, (size_t)(b0 + r) * ldx + c0);
 #pragma unroll
-            for (int i = 0; i < K - 1; ++i) sr[r][i] = ld16(state, ((size_t)(b0 + r) * (K - 1) + i) * C + c0);
+            for (int i = 0; i < K - 1; ++i) sr[r][i] = ld16(state, ((size_t)at[r] * (K - 1) + i) * C + c0);
         }
+    if constexpr (POOLED) {
+        unsigned bad = 0;
+        for (int i = tid; i < b0 + kDecRows - 1; i += kConvThreads) {
+            const int32_t other = i < B ? slots[i] : -1;
+#pragma unroll
+            for (int r = 0; r < kDecRows; ++r) bad |= (i < b0 + r && other == at[r] ? 1u : 0u) << r;
+        }
+#pragma unroll
+        for (int r = 0; r < kDecRows; ++r) {
+            const bool off = __syncthreads_or((int)(bad >> r & 1u)) || at[r] >= num_slots;
+            if (off && at[r] >= 0) {
+                if (tid == 0) report_status(status, GDN_ERR_INVALID_ARG);
+                at[r] = -1;
+            }
+        }
+    }
     f2_t w2[K][4];
     load_weights<K>(w, cb, C, wsm, w2);
     if (!active) return;
@@ -297,7 +320,7 @@ short_conv_decode_kernel(const void *__restrict__ x, int64_t ldx, const float *_
 #pragma unroll
     for (int r = 0; r < kDecRows; ++r) {
         const int bi = b0 + r;
-        if (bi >= B) break;
+        if (at[r] < 0) continue;
         f2_t h2[K > 1 ? K - 1 : 1][4], x2[4];
 #pragma unroll
         for (int i = 0; i < K - 1; ++i) unpack8(sr[r][i], h2[i]);
@@ -305,7 +328,7 @@ short_conv_decode_kernel(const void *__restrict__ x, int64_t ldx, const float *_
         *reinterpret_cast<uint4 *>(ycol + (size_t)bi * pitch) = conv_silu8<K>(w2, h2, x2);
 #pragma unroll
         for (int i = 0; i < K - 1; ++i)
-            st16(state, ((size_t)bi * (K - 1) + i) * C + c0, i + 1 < K - 1 ? sr[r][i + 1 < K - 1 ? i + 1 : 0] : xr[r]);
+            st16(state, ((size_t)at[r] * (K - 1) + i) * C + c0, i + 1 < K - 1 ? sr[r][i + 1 < K - 1 ? i + 1 : 0] : xr[r]);
     }
 }
 
@@ -349,10 +372,14 @@ template <int K>
 cudaError_t launch_conv_k(const ConvArgs &a, cudaStream_t st) {
     const int n_cblk = (a.C / 8 + kConvThreads - 1) / kConvThreads;
     const Planes pl = make_planes(a);
-    if (a.decode)
-        return launch_pdl(short_conv_decode_kernel<K>,
-                          dim3((unsigned)n_cblk, (unsigned)((a.num_seqs + kDecRows - 1) / kDecRows)),
-                          dim3(kConvThreads), 0, st, a.x, a.ldx, a.w, a.num_seqs, a.C, a.final_state, a.y, pl);
+    if (a.decode) {
+        const dim3 grid((unsigned)n_cblk, (unsigned)((a.num_seqs + kDecRows - 1) / kDecRows));
+        if (a.slots)
+            return launch_pdl(short_conv_decode_kernel<K, true>, grid, dim3(kConvThreads), 0, st, a.x, a.ldx, a.w,
+                              a.num_seqs, a.C, a.final_state, a.y, pl, a.slots, a.num_slots, a.status);
+        return launch_pdl(short_conv_decode_kernel<K, false>, grid, dim3(kConvThreads), 0, st, a.x, a.ldx, a.w,
+                          a.num_seqs, a.C, a.final_state, a.y, pl, a.slots, a.num_slots, a.status);
+    }
     if (a.T > 0) {
         const int grid = conv_grid<K>(n_cblk, a.T);
         if (grid < 0) return cudaErrorUnknown;

@@ -164,6 +164,66 @@ struct Q4kGemmArgs {
 };
 cudaError_t launch_q4k_gemm(const Q4kGemmArgs &g, cudaStream_t st);
 
+// FP8 encode of x [rows, K] (rows of ldx elements): 1 x 128 blocks, or 128 x 128 ones of a weight.
+struct Fp8QuantArgs {
+    const void *x;
+    int64_t ldx;
+    bool in_bf16, weight;
+    int32_t rows, K;
+    uint8_t *xq;                 // [rows, K] E4M3
+    float *xs;                   // [rows, ceil(K / 128)], weight: [ceil(rows / 128), ceil(K / 128)]
+};
+cudaError_t launch_fp8_quantize(const Fp8QuantArgs &a, cudaStream_t st);
+
+struct Fp8TailArgs {
+    const void *o, *z;           // [M, Hv, D]
+    const float *w;
+    float eps;
+    int32_t M, Hv, D;
+    bool in_bf16;
+    uint8_t *xq;                 // [M, Hv * D] E4M3
+    float *xs;                   // [M, ceil(Hv * D / 128)]
+};
+cudaError_t launch_gated_rmsnorm_fp8(const Fp8TailArgs &t, cudaStream_t st);
+
+// y [M, N] = (aq as) (bq bs)^T, E4M3 codes with fp32 scales per 1 x 128 (a) and 128 x 128 (b) block.
+struct Fp8GemmArgs {
+    const uint8_t *aq;
+    const float *as;
+    const uint8_t *bq;
+    const float *bs;
+    int32_t M, N, K;
+    bool out_bf16;
+    void *y;
+    int *status;
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st);
+
+// One decode token per row (d = 128, bf16) on states in a pool of slots; with xq set, the gated tail in FP8.
+struct PooledDecodeArgs {
+    const void *q, *k, *v;       // [B, Hk, 128], [B, Hk, 128], [B, Hv, 128] bf16
+    const void *a, *b;           // [B, Hv], rows of ldg elements, bf16 or fp32
+    int64_t ldg;
+    bool gate_bf16;
+    const float *A_log, *dt_bias;
+    int32_t B, Hk, Hv;
+    float scale;
+    int32_t l2norm;
+    float *pool;                 // [num_slots, Hv, 128, 128] fp32, in place
+    int32_t num_slots;
+    const int32_t *slots;        // [B]
+    void *o;                     // [B, Hv, 128] or null
+    bool out_bf16;
+    const void *z;               // [B, Hv * 128] bf16, rows of ldz elements
+    int64_t ldz;
+    const float *norm_w;         // [128]
+    float eps;
+    uint8_t *xq;                 // [B, Hv * 128] E4M3 or null (no tail)
+    float *xs;                   // [B, Hv]
+    int *status;
+};
+cudaError_t launch_decode_pooled(const PooledDecodeArgs &d, cudaStream_t st);
+
 struct ConvArgs {
     const void *x;               // bf16 rows of ldx elements; channels [0, C) are convolved
     int64_t ldx;
@@ -176,6 +236,9 @@ struct ConvArgs {
     int32_t part_end[4];
     int32_t n_parts;
     bool decode;                 // one token per sequence, state shifted in place
+    const int32_t *slots;        // decode: device [num_seqs] slots of final_state, a pool of num_slots, or null
+    int32_t num_slots;
+    int *status;
 };
 cudaError_t launch_short_conv(const ConvArgs &a, cudaStream_t st);
 

@@ -1,0 +1,296 @@
+// The single-token gated delta rule on states that lie in a pool of slots (one slot per live request, batch
+// rows naming theirs), plain or with the gated tail and its FP8 encoding in the same kernel:
+//     S = alpha S + beta (v - alpha S k^) k^^T,  o = S q^,  S = pool[slots[row], head]  (128 x 128 fp32, in place),
+// "Why Gated DeltaNet Survives 4-Bit Quantization" (abstract, mechanisms ii-iii); tail: "Red Lite dev15d -
+// DeltaNet gated tail", Pinned graph semantics, steps 1-5.
+//
+// HBM-bound: 128 KB of state traffic and about 8 operations a state value per (row, head). Persistent, one CTA
+// per SM over an equal share of the (row, head) items; a producer warp brings each item's 64 KB state and its
+// q, k, v, z rows into a three-stage ring by bulk copies, so loads stay in flight while items are
+// computed, written back and encoded:
+//   warps 0-7  the state from the stage into registers (8 lanes a row, 4 rows a thread, the layout and
+//              arithmetic of gdn_recurrent128_kernel, so o and S equal gdn_decode_step's bit for bit), the
+//              stage released at once, the update, S stored straight to the pool, o to shared memory;
+//              warp i % 8 then finishes item i's o row (tail and encode, or the plain store) while the
+//              others go on;
+//   warp 8     slots, bulk copies, gates.
+// A row with a negative slot is passed over (its outputs stay as they are); so is a row whose slot is not
+// below num_slots or is named by an earlier row, and the status word then reads GDN_ERR_INVALID_ARG.
+// Every wait is bounded; an expired one records GDN_ERR_TIMEOUT and the warp ends.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kPoolStages = 3;
+constexpr int kPoolWarps = 8;
+constexpr int kPoolThreads = 32 * (kPoolWarps + 1);
+constexpr uint32_t kStateBytes = kD * kD * 4;
+constexpr uint32_t kRowBytes = kD * 2;
+constexpr unsigned kAll = 0xffffffffu;
+
+struct PoolMeta {
+    int32_t row, head, slot;   // row < 0: no more items
+    float alpha, beta;
+};
+struct PoolSmem {
+    float state[kPoolStages][kD * kD];
+    __nv_bfloat16 q[kPoolStages][kD], k[kPoolStages][kD], v[kPoolStages][kD], z[kPoolStages][kD];
+    float o[2][kD];
+    PoolMeta meta[kPoolStages];
+    uint64_t full[kPoolStages], empty[kPoolStages], o_full[2], o_empty[2];
+};
+constexpr int kPoolSmem = (int)sizeof(PoolSmem) + 128;
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ float pool_dot16(const f2_t (&a)[8], const f2_t (&b)[8]) {
+    f2_t acc = mul2(a[0], b[0]);
+#pragma unroll
+    for (int c = 1; c < 8; ++c) acc = fma2(a[c], b[c], acc);
+    return f2lo(acc) + f2hi(acc);
+}
+// The sum over a row group of 8 lanes of four values: lanes whose bits 2 and 1 are (p >> 1, p & 1) get value p.
+__device__ __forceinline__ float pool_sum4(const float (&x)[4], int l8) {
+    const bool b2 = (l8 & 4) != 0, b1 = (l8 & 2) != 0;
+    const float r0 = __shfl_xor_sync(kAll, b2 ? x[0] : x[2], 4);
+    const float r1 = __shfl_xor_sync(kAll, b2 ? x[1] : x[3], 4);
+    const float k0 = (b2 ? x[2] : x[0]) + r0, k1 = (b2 ? x[3] : x[1]) + r1;
+    float v = (b1 ? k1 : k0) + __shfl_xor_sync(kAll, b1 ? k0 : k1, 2);
+    v += __shfl_xor_sync(kAll, v, 1);
+    return v;
+}
+// Columns 32 j + 4 l8 + e of a staged bf16 row as 8 pairs.
+__device__ __forceinline__ void pool_cols16(const __nv_bfloat16 *row, int l8, f2_t (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(row + 32 * j + 4 * l8);
+        x[2 * j] = bf16x2_to_f2(u.x);
+        x[2 * j + 1] = bf16x2_to_f2(u.y);
+    }
+}
+
+__device__ __forceinline__ float gate_at(const void *p, bool bf16, int64_t idx) {
+    return bf16 ? load1<true>(p, idx) : load1<false>(p, idx);
+}
+
+// One lane waits (bounded), the warp learns the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int lane, int *status) {
+    bool ok = true;
+    if (lane == 0) ok = mbar_wait(bar, parity, status);
+    return __shfl_sync(kAll, ok, 0);
+}
+
+template <bool TAIL>
+__global__ void __launch_bounds__(kPoolThreads, 1)
+gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
+    pdl_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    PoolSmem &sm = *reinterpret_cast<PoolSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (tid == 0) {
+        for (int s = 0; s < kPoolStages; ++s) {
+            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.empty[s], kPoolWarps);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.o_full[b], kPoolWarps);
+            mbar_init(&sm.o_empty[b], 1);
+        }
+        fence_barrier_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    const int Hv = d.Hv;
+
+    if (warp == kPoolWarps) {
+        const int64_t items = (int64_t)d.B * Hv;
+        const int first = (int)(items * blockIdx.x / gridDim.x), last = (int)(items * (blockIdx.x + 1) / gridDim.x);
+        const int group = Hv / d.Hk;
+        int it = 0, row = -1, slot = -1;
+        bool ok = true;
+        for (int item = first; item < last && ok; ++item) {
+            if (item / Hv != row) {
+                row = item / Hv;
+                slot = d.slots[row];
+                bool seen = false;
+                for (int i = lane; i < row; i += 32) seen |= d.slots[i] == slot;
+                seen = __any_sync(kAll, seen);
+                if (slot >= 0 && (slot >= d.num_slots || seen)) {
+                    if (lane == 0) report_status(d.status, GDN_ERR_INVALID_ARG);
+                    slot = -1;
+                }
+            }
+            if (slot < 0) {
+                item = (row + 1) * Hv - 1;   // the next row
+                continue;
+            }
+            const int h = item - row * Hv, s = it % kPoolStages;
+            ok = warp_wait(&sm.empty[s], (uint32_t)(((it / kPoolStages) & 1) ^ 1), lane, d.status);
+            if (!ok) break;
+            if (lane == 0) {
+                const int64_t vrow = ((int64_t)row * Hv + h) * kD, krow = ((int64_t)row * d.Hk + h / group) * kD;
+                float g, beta;
+                gdn_gates(gate_at(d.a, d.gate_bf16, row * d.ldg + h), gate_at(d.b, d.gate_bf16, row * d.ldg + h), d.A_log[h],
+                          d.dt_bias[h], g, beta);
+                sm.meta[s] = {row, h, slot, expf(g), beta};
+                mbar_arrive_expect_tx(&sm.full[s], kStateBytes + (TAIL ? 4 : 3) * kRowBytes);
+                bulk_load(sm.state[s], d.pool + ((int64_t)slot * Hv + h) * kD * kD, kStateBytes, &sm.full[s]);
+                bulk_load(sm.k[s], reinterpret_cast<const __nv_bfloat16 *>(d.k) + krow, kRowBytes, &sm.full[s]);
+                bulk_load(sm.q[s], reinterpret_cast<const __nv_bfloat16 *>(d.q) + krow, kRowBytes, &sm.full[s]);
+                bulk_load(sm.v[s], reinterpret_cast<const __nv_bfloat16 *>(d.v) + vrow, kRowBytes, &sm.full[s]);
+                if constexpr (TAIL)
+                    bulk_load(sm.z[s], reinterpret_cast<const __nv_bfloat16 *>(d.z) + row * d.ldz + h * kD, kRowBytes,
+                              &sm.full[s]);
+            }
+            __syncwarp();
+            ++it;
+        }
+        // the end mark, and before the warp ends every copy it armed has landed
+        const int s_end = it % kPoolStages;
+        if (ok) ok = warp_wait(&sm.empty[s_end], (uint32_t)(((it / kPoolStages) & 1) ^ 1), lane, d.status);
+        if (lane == 0) {
+            for (int s = 0; s < kPoolStages && s < it; ++s) {
+                const int at = it - 1 - ((it - 1 - s) % kPoolStages);
+                mbar_wait(&sm.full[s], (uint32_t)((at / kPoolStages) & 1), d.status);
+            }
+            if (ok) {
+                sm.meta[s_end].row = -1;
+                mbar_arrive(&sm.full[s_end]);
+            }
+        }
+        return;
+    }
+
+    const int l8 = tid & 7, rbase = (tid >> 7) * 64 + ((tid & 127) >> 3), gbase = lane & ~7, col = (lane & 15) * 8;
+    f2_t w2[4];
+    if constexpr (TAIL) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w2[j] = f2(d.norm_w[col + 2 * j], d.norm_w[col + 2 * j + 1]);
+    }
+    for (int it = 0;; ++it) {
+        const int s = it % kPoolStages, ob = it & 1;
+        if (!warp_wait(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), lane, d.status)) break;
+        const PoolMeta m = sm.meta[s];
+        if (m.row < 0) break;
+        const bool finisher = warp == it % kPoolWarps;
+
+        f2_t st[4][8], k2[8], q2[8];
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 x = *reinterpret_cast<const float4 *>(&sm.state[s][(rbase + 16 * p) * kD + 32 * j + 4 * l8]);
+                st[p][2 * j] = f2(x.x, x.y);
+                st[p][2 * j + 1] = f2(x.z, x.w);
+            }
+        pool_cols16(sm.k[s], l8, k2);
+        pool_cols16(sm.q[s], l8, q2);
+        float vv[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) vv[p] = __bfloat162float(sm.v[s][rbase + 16 * p]);
+        uint4 zu = make_uint4(0u, 0u, 0u, 0u);
+        if (TAIL && finisher) zu = *reinterpret_cast<const uint4 *>(&sm.z[s][col]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.empty[s]);
+
+        float kn = 1.0f, qn = d.scale;
+        if (d.l2norm) {
+            const float ks = group_sum<8>(pool_dot16(k2, k2)), qs = group_sum<8>(pool_dot16(q2, q2));
+            kn = rsqrtf(ks + 1e-6f);
+            qn = rsqrtf(qs + 1e-6f) * d.scale;
+        }
+        float part[4], sk[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) part[p] = pool_dot16(st[p], k2);
+        const float skt = pool_sum4(part, l8);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) sk[p] = __shfl_sync(kAll, skt, gbase + 4 * (p >> 1) + 2 * (p & 1));
+        const f2_t a2 = f2(m.alpha, m.alpha);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const float u = m.beta * (vv[p] - m.alpha * kn * sk[p]) * kn;
+            const f2_t u2 = f2(u, u);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) st[p][c] = fma2(a2, st[p][c], mul2(u2, k2[c]));
+        }
+        float *out = d.pool + ((int64_t)m.slot * Hv + m.head) * kD * kD + rbase * kD + 4 * l8;
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                __stcs(reinterpret_cast<float4 *>(out + 16 * p * kD + 32 * j),
+                       make_float4(f2lo(st[p][2 * j]), f2hi(st[p][2 * j]), f2lo(st[p][2 * j + 1]), f2hi(st[p][2 * j + 1])));
+#pragma unroll
+        for (int p = 0; p < 4; ++p) part[p] = pool_dot16(st[p], q2);
+        const float ot = pool_sum4(part, l8) * qn;
+        // this buffer's row of two items ago has been finished
+        if (!warp_wait(&sm.o_empty[ob], (uint32_t)(((it >> 1) & 1) ^ 1), lane, d.status)) break;
+        if ((l8 & 1) == 0) sm.o[ob][rbase + 16 * (2 * ((l8 >> 2) & 1) + ((l8 >> 1) & 1))] = ot;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_full[ob]);
+        if (!finisher) continue;
+
+        if (!warp_wait(&sm.o_full[ob], (uint32_t)((it >> 1) & 1), lane, d.status)) break;
+        const int64_t at = ((int64_t)m.row * Hv + m.head) * kD;
+        const float4 oa = *reinterpret_cast<const float4 *>(&sm.o[ob][col]), oc = *reinterpret_cast<const float4 *>(&sm.o[ob][col + 4]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.o_empty[ob]);
+        if (d.o && lane < 16) {
+            const float x[8] = {oa.x, oa.y, oa.z, oa.w, oc.x, oc.y, oc.z, oc.w};
+            if (d.out_bf16) store8<true>(d.o, at + col, x);
+            else store8<false>(d.o, at + col, x);
+        }
+        if constexpr (TAIL) {
+            // lanes 16-31 repeat the row, their results unused
+            const f2_t o2[4] = {f2(oa.x, oa.y), f2(oa.z, oa.w), f2(oc.x, oc.y), f2(oc.z, oc.w)};
+            const f2_t z2[4] = {bf16x2_to_f2(zu.x), bf16x2_to_f2(zu.y), bf16x2_to_f2(zu.z), bf16x2_to_f2(zu.w)};
+            f2_t y2[4];
+            gated_row8<16>(o2, z2, w2, 1.0f / (float)kD, d.eps, y2);
+            float amax = 0.0f, r;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(f2lo(y2[j])), fabsf(f2hi(y2[j]))));
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
+            const float sc = fp8_block_scale(amax, r);
+            if (lane < 16)
+                *reinterpret_cast<uint2 *>(d.xq + at + col) =
+                    make_uint2(fp8_pack4(f2lo(y2[0]), f2hi(y2[0]), f2lo(y2[1]), f2hi(y2[1]), r),
+                               fp8_pack4(f2lo(y2[2]), f2hi(y2[2]), f2lo(y2[3]), f2hi(y2[3]), r));
+            if (lane == 0) d.xs[at / kD] = sc;
+        }
+    }
+}
+
+template <bool TAIL>
+cudaError_t launch_pooled_t(const PooledDecodeArgs &d, cudaStream_t st) {
+    static PerDevice<int> sm_count;   // the shared-memory attribute is set per device alongside
+    int sms = 0;
+    const cudaError_t e = sm_count.get(
+        [](int dev, int &r) {
+            cudaError_t x = cudaFuncSetAttribute(gdn_decode128_pooled_kernel<TAIL>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kPoolSmem);
+            if (x == cudaSuccess) x = cudaDeviceGetAttribute(&r, cudaDevAttrMultiProcessorCount, dev);
+            return x;
+        },
+        &sms);
+    if (e != cudaSuccess) return e;
+    const int64_t items = (int64_t)d.B * d.Hv;
+    return launch_pdl(gdn_decode128_pooled_kernel<TAIL>, dim3((unsigned)(items < sms ? items : sms)), dim3(kPoolThreads),
+                      kPoolSmem, st, d);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_pooled(const PooledDecodeArgs &d, cudaStream_t st) {
+    return d.xq ? launch_pooled_t<true>(d, st) : launch_pooled_t<false>(d, st);
+}
+
+}  // namespace gdn

@@ -1,5 +1,5 @@
 /*
- * gdn.h - C ABI of the Gated DeltaNet token mixer and its NVFP4 gated tail on B200 (sm_100a).
+ * gdn.h - C ABI of the Gated DeltaNet token mixer and its NVFP4 or FP8 gated tail on B200 (sm_100a).
  *
  * The operations (page title, section):
  *   [GDN]  "Why Gated DeltaNet Survives 4-Bit Quantization: NVFP4 W4A4 for the Recurrent
@@ -284,6 +284,71 @@ GDN_API gdn_status nvfp4_fused_col_alpha(const int32_t *widths, const float *mod
 GDN_API gdn_status q4k_gemm(const void *a, const uint8_t *w, int32_t M, int32_t N, int32_t K, gdn_dtype out_dtype,
                             void *y, gdn_stream_t stream);
 
+/* ------------------------------------------------------------ FP8 encode ----
+ * E4M3 codes with one fp32 scale per block of 128 values along K. For the block's largest magnitude
+ * amax (a NaN is passed over), in fp32:
+ *   s = max(amax / 448, 2^-126);  code_j = E4M3(x_j * (1 / s)) (nearest, ties to even, saturating at
+ *   448; a NaN stays NaN). Decoded value: E4M3(code) * s.
+ * An infinity makes its block's scale infinite, and the block decodes to NaN.
+ * x [M, K] in `in_dtype`, rows of ldx >= K elements (16-byte aligned rows: ldx % 8 == 0 for bf16,
+ * % 4 for fp32), so x can be a column block of a wider matrix.
+ * fp8_quantize_act: blocks of 1 x 128; xq [M, K] E4M3 codes, xs [M, ceil(K / 128)] fp32.
+ * fp8_quantize_weight: blocks of 128 x 128; wq [N, K], ws [ceil(N / 128), ceil(K / 128)].
+ * A last block past the edge of the matrix holds what is left. Supported: K % 16 == 0, M, N >= 0,
+ * M * ceil(K / 128) < 2^31. */
+GDN_API gdn_status fp8_quantize_act(const void *x, int64_t ldx, gdn_dtype in_dtype, int32_t M, int32_t K,
+                                    uint8_t *xq, float *xs, gdn_stream_t stream);
+GDN_API gdn_status fp8_quantize_weight(const void *w, int64_t ldw, gdn_dtype in_dtype, int32_t N, int32_t K,
+                                       uint8_t *wq, float *ws, gdn_stream_t stream);
+
+/* The gated tail ([TAIL] steps 1-5, as gdn_gated_rmsnorm_silu) with its FP8 encode fused in: y is formed
+ * in fp32 and encoded as fp8_quantize_act would encode that fp32 tensor (the two paths agree bit for
+ * bit; no rounding to bf16 between). K = Hv * Dv; xq [M, K] E4M3 codes, xs [M, ceil(K / 128)] fp32.
+ * Supported: Dv in {16, 32, 64, 128}; M * ceil(K / 128) < 2^31. */
+GDN_API gdn_status gdn_gated_rmsnorm_silu_fp8(const void *o, const void *z, const float *weight, float eps,
+                                              int32_t M, int32_t Hv, int32_t Dv, gdn_dtype in_dtype,
+                                              uint8_t *xq, float *xs, gdn_stream_t stream);
+
+/* ------------------------------------------------------------ FP8 GEMM ----
+ * y[m, n] = sum over blocks B of 128 along K of as[m, B] bs[n / 128, B] sum_{k in B} a[m, k] b[n, k]
+ * with fp32 accumulation; the sum inside a block on the FP8 tensor cores.
+ * aq [M, K], as [M, ceil(K / 128)]: activations as fp8_quantize_act writes them; bq [N, K] (K contiguous),
+ * bs [ceil(N / 128), ceil(K / 128)]: a weight as fp8_quantize_weight writes it; y [M, N] in `out_dtype`.
+ * Modules stacked along N need no factors of their own where each starts at a multiple of 128.
+ * Supported: K % 16 == 0, N % 16 == 0, M >= 0, M <= 128 * 65535. */
+GDN_API gdn_status fp8_gemm(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs, int32_t M,
+                            int32_t N, int32_t K, gdn_dtype out_dtype, void *y, gdn_stream_t stream);
+
+/* ------------------------------------------------- decode on a pool of states ----
+ * gdn_decode_step for a server that keeps each request's state in one slot of a pool: row b of the batch
+ * reads and updates slot slots[b] of state_pool [num_slots, Hv, 128, 128] fp32.
+ * slots  device int32 [B]. A negative entry marks a padded row: its state and its outputs stay as they
+ *        are. So do those of a row whose entry is not below num_slots, or is also an earlier row's; the
+ *        device status word then reads GDN_ERR_INVALID_ARG (gdn_get_device_status).
+ * a, b   gate pre-activations in `gate_dtype`, rows of ldg elements (ldg >= Hv), so they can be column
+ *        blocks of a projection's output. q, k, v, o as gdn_decode_step.
+ * Supported: Dk == Dv == 128, bf16 q, k, v; Hv % Hk == 0; B >= 0, B * Hv < 2^31.
+ * o and the states equal gdn_decode_step's on the same rows bit for bit. */
+GDN_API gdn_status gdn_decode_step_pooled(const void *q, const void *k, const void *v, const void *a, const void *b,
+                                          int64_t ldg, gdn_dtype gate_dtype, const float *A_log,
+                                          const float *dt_bias, int32_t B, int32_t Hk, int32_t Hv, int32_t Dk,
+                                          int32_t Dv, float scale, int32_t qk_l2norm, gdn_dtype in_dtype,
+                                          float *state_pool, int32_t num_slots, const int32_t *slots, void *o,
+                                          gdn_dtype out_dtype, gdn_stream_t stream);
+
+/* gdn_decode_step_pooled fused with the gated tail and its FP8 encode: the bytes of gdn_decode_step_pooled
+ * (fp32 o) followed by gdn_gated_rmsnorm_silu_fp8 on that o. z [B, Hv * 128] bf16, rows of ldz
+ * elements (ldz % 8 == 0); norm_weight [128] fp32; xq [B, Hv * 128] E4M3 codes, xs [B, Hv] fp32 (one
+ * block per head); o [B, Hv, 128] bf16 is also written when not NULL. */
+GDN_API gdn_status gdn_decode_step_pooled_gated_fp8(const void *q, const void *k, const void *v, const void *a,
+                                                    const void *b, int64_t ldg, gdn_dtype gate_dtype,
+                                                    const float *A_log, const float *dt_bias, int32_t B, int32_t Hk,
+                                                    int32_t Hv, int32_t Dk, int32_t Dv, float scale,
+                                                    int32_t qk_l2norm, gdn_dtype in_dtype, float *state_pool,
+                                                    int32_t num_slots, const int32_t *slots, const void *z,
+                                                    int64_t ldz, const float *norm_weight, float eps, uint8_t *xq,
+                                                    float *xs, void *o, gdn_stream_t stream);
+
 /* ------------------------------------------------------ short convolution ----
  * [WALK]: the causal short convolution + SiLU on the layer's q, k, v channels before the scan:
  *   y[t, c] = SiLU(sum_{j<K} weight[c, j] x[t - (K - 1) + j, c])
@@ -321,6 +386,15 @@ GDN_API gdn_status gdn_short_conv1d_silu_decode(const void *x, int64_t ldx, cons
                                                 int32_t B, int32_t C, int32_t K, void *conv_state,
                                                 void *y, const int32_t *part_widths, int32_t n_parts,
                                                 gdn_stream_t stream);
+
+/* gdn_short_conv1d_silu_decode on a pool of carried states: row b reads and shifts slot slots[b] of
+ * conv_pool bf16 [num_slots, K - 1, C]; slots as for gdn_decode_step_pooled (a padded row's y and state
+ * stay as they are). conv_pool must not overlap x or y. Supported: as gdn_short_conv1d_silu_decode,
+ * B <= 4 * 65535. */
+GDN_API gdn_status gdn_short_conv1d_silu_decode_pooled(const void *x, int64_t ldx, const float *weight, int32_t B,
+                                                       int32_t C, int32_t K, void *conv_pool, int32_t num_slots,
+                                                       const int32_t *slots, void *y, const int32_t *part_widths,
+                                                       int32_t n_parts, gdn_stream_t stream);
 
 /* ------------------------------------------------- allocation-free prefill ----
  * No counterpart in the pages this library follows. For callers that cannot allocate device
