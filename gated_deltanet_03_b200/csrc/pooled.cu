@@ -8,12 +8,13 @@
 // per SM over an equal share of the (row, head) items; a producer warp brings each item's 64 KB state and its
 // q, k, v, z rows into a three-stage ring by bulk copies, so loads stay in flight while items are
 // computed, written back and encoded:
-//   warps 0-7  the state from the stage into registers (8 lanes a row, 4 rows a thread, the layout and
-//              arithmetic of gdn_recurrent128_kernel, so o and S equal gdn_decode_step's bit for bit), the
-//              stage released at once, the update, S stored straight to the pool, o to shared memory;
-//              warp i % 8 then finishes item i's o row (tail and encode, or the plain store) while the
-//              others go on;
-//   warp 8     slots, bulk copies, gates.
+//   warps 0-7   the state from the stage into registers (8 lanes a row, 4 rows a thread, the layout and
+//               arithmetic of gdn_recurrent128_kernel, so o and S equal gdn_decode_step's bit for bit), the
+//               stage released at once, the update, S stored straight to the pool, o to shared memory;
+//   warp 8      slots, bulk copies, gates;
+//   warps 9-10  item i's o row on warp 9 + i % 2 (tail and encode, or the plain store). Its chain of
+//               reductions and divisions takes longer than the update; done in turn by the update's own warps
+//               it held up every item's last row (6.5 us an item against 3 us of HBM time).
 // A row with a negative slot is passed over (its outputs stay as they are); so is a row whose slot is not
 // below num_slots or is named by an earlier row, and the status word then reads GDN_ERR_INVALID_ARG.
 // Every wait is bounded; an expired one records GDN_ERR_TIMEOUT and the warp ends.
@@ -26,7 +27,9 @@ namespace {
 constexpr int kD = 128;
 constexpr int kPoolStages = 3;
 constexpr int kPoolWarps = 8;
-constexpr int kPoolThreads = 32 * (kPoolWarps + 1);
+constexpr int kPoolFinishers = 2;
+constexpr int kPoolRows = 4;               // o rows between the update and the finishers
+constexpr int kPoolThreads = 32 * (kPoolWarps + 1 + kPoolFinishers);
 constexpr uint32_t kStateBytes = kD * kD * 4;
 constexpr uint32_t kRowBytes = kD * 2;
 constexpr unsigned kAll = 0xffffffffu;
@@ -38,9 +41,9 @@ struct PoolMeta {
 struct PoolSmem {
     float state[kPoolStages][kD * kD];
     __nv_bfloat16 q[kPoolStages][kD], k[kPoolStages][kD], v[kPoolStages][kD], z[kPoolStages][kD];
-    float o[2][kD];
+    float o[kPoolRows][kD];
     PoolMeta meta[kPoolStages];
-    uint64_t full[kPoolStages], empty[kPoolStages], o_full[2], o_empty[2];
+    uint64_t full[kPoolStages], empty[kPoolStages], o_full[kPoolRows], o_empty[kPoolRows];
 };
 constexpr int kPoolSmem = (int)sizeof(PoolSmem) + 128;
 
@@ -98,9 +101,9 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
     if (tid == 0) {
         for (int s = 0; s < kPoolStages; ++s) {
             mbar_init(&sm.full[s], 1);
-            mbar_init(&sm.empty[s], kPoolWarps);
+            mbar_init(&sm.empty[s], kPoolWarps + 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kPoolRows; ++b) {
             mbar_init(&sm.o_full[b], kPoolWarps);
             mbar_init(&sm.o_empty[b], 1);
         }
@@ -153,34 +156,77 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
             __syncwarp();
             ++it;
         }
-        // the end mark, and before the warp ends every copy it armed has landed
-        const int s_end = it % kPoolStages;
-        if (ok) ok = warp_wait(&sm.empty[s_end], (uint32_t)(((it / kPoolStages) & 1) ^ 1), lane, d.status);
+        // before the warp ends every copy it armed has landed; then one end mark for each finisher
         if (lane == 0) {
             for (int s = 0; s < kPoolStages && s < it; ++s) {
                 const int at = it - 1 - ((it - 1 - s) % kPoolStages);
                 mbar_wait(&sm.full[s], (uint32_t)((at / kPoolStages) & 1), d.status);
             }
-            if (ok) {
-                sm.meta[s_end].row = -1;
-                mbar_arrive(&sm.full[s_end]);
+            for (int e = it; e < it + kPoolFinishers && ok; ++e) {
+                const int s = e % kPoolStages;
+                ok = mbar_wait(&sm.empty[s], (uint32_t)(((e / kPoolStages) & 1) ^ 1), d.status);
+                if (!ok) break;
+                sm.meta[s].row = -1;
+                mbar_arrive(&sm.full[s]);
             }
         }
         return;
     }
 
-    const int l8 = tid & 7, rbase = (tid >> 7) * 64 + ((tid & 127) >> 3), gbase = lane & ~7, col = (lane & 15) * 8;
-    f2_t w2[4];
-    if constexpr (TAIL) {
+    if (warp > kPoolWarps) {
+        const int col = (lane & 15) * 8;   // lanes 16-31 repeat the row, their results unused
+        f2_t w2[4];
+        if constexpr (TAIL) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w2[j] = f2(d.norm_w[col + 2 * j], d.norm_w[col + 2 * j + 1]);
+            for (int j = 0; j < 4; ++j) w2[j] = f2(d.norm_w[col + 2 * j], d.norm_w[col + 2 * j + 1]);
+        }
+        for (int it = warp - kPoolWarps - 1;; it += kPoolFinishers) {
+            const int s = it % kPoolStages, ob = it % kPoolRows;
+            if (!warp_wait(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), lane, d.status)) break;
+            const int row = sm.meta[s].row, head = sm.meta[s].head;
+            if (row < 0) break;
+            uint4 zu = make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (TAIL) zu = *reinterpret_cast<const uint4 *>(&sm.z[s][col]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.empty[s]);
+            if (!warp_wait(&sm.o_full[ob], (uint32_t)((it / kPoolRows) & 1), lane, d.status)) break;
+            const float4 oa = *reinterpret_cast<const float4 *>(&sm.o[ob][col]);
+            const float4 oc = *reinterpret_cast<const float4 *>(&sm.o[ob][col + 4]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.o_empty[ob]);
+            const int64_t at = ((int64_t)row * Hv + head) * kD;
+            if (d.o && lane < 16) {
+                const float x[8] = {oa.x, oa.y, oa.z, oa.w, oc.x, oc.y, oc.z, oc.w};
+                if (d.out_bf16) store8<true>(d.o, at + col, x);
+                else store8<false>(d.o, at + col, x);
+            }
+            if constexpr (TAIL) {
+                const f2_t o2[4] = {f2(oa.x, oa.y), f2(oa.z, oa.w), f2(oc.x, oc.y), f2(oc.z, oc.w)};
+                const f2_t z2[4] = {bf16x2_to_f2(zu.x), bf16x2_to_f2(zu.y), bf16x2_to_f2(zu.z), bf16x2_to_f2(zu.w)};
+                f2_t y2[4];
+                gated_row8<16>(o2, z2, w2, 1.0f / (float)kD, d.eps, y2);
+                float amax = 0.0f, r;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(f2lo(y2[j])), fabsf(f2hi(y2[j]))));
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
+                const float sc = fp8_block_scale(amax, r);
+                if (lane < 16)
+                    *reinterpret_cast<uint2 *>(d.xq + at + col) =
+                        make_uint2(fp8_pack4(f2lo(y2[0]), f2hi(y2[0]), f2lo(y2[1]), f2hi(y2[1]), r),
+                                   fp8_pack4(f2lo(y2[2]), f2hi(y2[2]), f2lo(y2[3]), f2hi(y2[3]), r));
+                if (lane == 0) d.xs[at / kD] = sc;
+            }
+        }
+        return;
     }
+
+    const int l8 = tid & 7, rbase = (tid >> 7) * 64 + ((tid & 127) >> 3), gbase = lane & ~7;
     for (int it = 0;; ++it) {
-        const int s = it % kPoolStages, ob = it & 1;
+        const int s = it % kPoolStages, ob = it % kPoolRows;
         if (!warp_wait(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), lane, d.status)) break;
         const PoolMeta m = sm.meta[s];
         if (m.row < 0) break;
-        const bool finisher = warp == it % kPoolWarps;
 
         f2_t st[4][8], k2[8], q2[8];
 #pragma unroll
@@ -196,8 +242,6 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
         float vv[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) vv[p] = __bfloat162float(sm.v[s][rbase + 16 * p]);
-        uint4 zu = make_uint4(0u, 0u, 0u, 0u);
-        if (TAIL && finisher) zu = *reinterpret_cast<const uint4 *>(&sm.z[s][col]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.empty[s]);
 
@@ -231,41 +275,11 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
 #pragma unroll
         for (int p = 0; p < 4; ++p) part[p] = pool_dot16(st[p], q2);
         const float ot = pool_sum4(part, l8) * qn;
-        // this buffer's row of two items ago has been finished
-        if (!warp_wait(&sm.o_empty[ob], (uint32_t)(((it >> 1) & 1) ^ 1), lane, d.status)) break;
+        // the row that this buffer held has been finished
+        if (!warp_wait(&sm.o_empty[ob], (uint32_t)(((it / kPoolRows) & 1) ^ 1), lane, d.status)) break;
         if ((l8 & 1) == 0) sm.o[ob][rbase + 16 * (2 * ((l8 >> 2) & 1) + ((l8 >> 1) & 1))] = ot;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.o_full[ob]);
-        if (!finisher) continue;
-
-        if (!warp_wait(&sm.o_full[ob], (uint32_t)((it >> 1) & 1), lane, d.status)) break;
-        const int64_t at = ((int64_t)m.row * Hv + m.head) * kD;
-        const float4 oa = *reinterpret_cast<const float4 *>(&sm.o[ob][col]), oc = *reinterpret_cast<const float4 *>(&sm.o[ob][col + 4]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.o_empty[ob]);
-        if (d.o && lane < 16) {
-            const float x[8] = {oa.x, oa.y, oa.z, oa.w, oc.x, oc.y, oc.z, oc.w};
-            if (d.out_bf16) store8<true>(d.o, at + col, x);
-            else store8<false>(d.o, at + col, x);
-        }
-        if constexpr (TAIL) {
-            // lanes 16-31 repeat the row, their results unused
-            const f2_t o2[4] = {f2(oa.x, oa.y), f2(oa.z, oa.w), f2(oc.x, oc.y), f2(oc.z, oc.w)};
-            const f2_t z2[4] = {bf16x2_to_f2(zu.x), bf16x2_to_f2(zu.y), bf16x2_to_f2(zu.z), bf16x2_to_f2(zu.w)};
-            f2_t y2[4];
-            gated_row8<16>(o2, z2, w2, 1.0f / (float)kD, d.eps, y2);
-            float amax = 0.0f, r;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) amax = fmaxf(amax, fmaxf(fabsf(f2lo(y2[j])), fabsf(f2hi(y2[j]))));
-#pragma unroll
-            for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
-            const float sc = fp8_block_scale(amax, r);
-            if (lane < 16)
-                *reinterpret_cast<uint2 *>(d.xq + at + col) =
-                    make_uint2(fp8_pack4(f2lo(y2[0]), f2hi(y2[0]), f2lo(y2[1]), f2hi(y2[1]), r),
-                               fp8_pack4(f2lo(y2[2]), f2hi(y2[2]), f2lo(y2[3]), f2hi(y2[3]), r));
-            if (lane == 0) d.xs[at / kD] = sc;
-        }
     }
 }
 
