@@ -14,6 +14,18 @@
 //   warps 2-3  the factors as[m, B] bs[n0 / 128, B] of the tile's MT rows, sixteen K blocks at a time;
 //   warps 4-   one weight row per thread (two threads for MT = 128, half the columns each): accumulator
 //              -> registers, one FMA per value, and at the end the tile through shared memory to y.
+//
+// fp8_gemm_wide_kernel, for many tokens: SM pairs (tcgen05.mma.cta_group::2) on 256 x 256 tiles, tokens on the M
+// side, CTA r of a pair holding 128 token rows and half of the 256 weight rows, so that a K block costs each SM
+// 32 KB of loads for 512 cycles of MMA (a 128 x 128 tile on one SM: 32 KB for 256, and loads are what
+// bounds it). Persistent; the two accumulators take all of tensor memory, so that the MMAs of one K block
+// run while the block before is scaled and added by the eight promotion warps, 128 fp32 sums a thread
+// (register split by setmaxnreg: 128 x 56 + 256 x 224 = 384 x 168, the launch's own total).
+//   warp 0     TMA producer of this CTA's operands;   warp 1     (leader) MMA issue;
+//   warp 2     (peer) tells the leader that a stage's operands have landed here;
+//   warp 3     the factors as[m, B] bs[n / 128, B] of this CTA's rows, through shared memory;
+//   warps 4-11 one token row and half of the 256 columns per thread.
+//
 // Every barrier wait is bounded (gdn_debug_set_wait); an expired one records GDN_ERR_TIMEOUT, issued copies
 // and MMAs are waited for (bounded), tensor memory is freed and the CTA ends.
 #include "common.cuh"
@@ -71,6 +83,30 @@ __device__ __forceinline__ void f8_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 // Instruction descriptor: fp32 accumulation, E4M3 A and B (format 0), both K-major.
 __host__ __device__ constexpr uint32_t f8_idesc(int m, int n) {
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Wait for tensor-memory loads, tied to the registers of the last one so that no use of them moves above it.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; i += 16)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                          "+r"(r[i + 6]), "+r"(r[i + 7]), "+r"(r[i + 8]), "+r"(r[i + 9]), "+r"(r[i + 10]), "+r"(r[i + 11]),
+                          "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
+}
+
+// One lane of a whole warp. The warps that issue copies and MMAs run their loops with all lanes, the wait
+// included, and elect a lane around the instructions alone: the operands of those instructions are warp-uniform
+// registers, and from inside a one-lane branch each MMA took about 90 cycles to issue, more than it ran.
+__device__ __forceinline__ bool f8_elect() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+// The whole warp waits (bounded); false in every lane if any lane's wait ran out.
+__device__ __forceinline__ bool f8_warp_wait(uint64_t *bar, uint32_t parity, int *status) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
 // Four consecutive values of a row of y.
@@ -135,43 +171,53 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     pdl_wait();
 
     if (warp == 0) {
-        if (lane == 0) {
-            int i = 0;
-            for (; i < nkb; ++i) {
-                const int s = i % STAGES;
-                if (!mbar_wait(&empty[s], (uint32_t)(((i / STAGES) & 1) ^ 1), status)) break;
+        int i = 0;
+        for (int s = 0, ph = 1; i < nkb; ++i) {
+            if (!f8_warp_wait(&empty[s], (uint32_t)ph, status)) break;
+            if (f8_elect()) {
                 mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
                 tma_load_2d(tile_w(s), &map_w, &full[s], (kb0 + i) * 128, n0);
                 tma_load_2d(tile_x(s), &map_x, &full[s], (kb0 + i) * 128, m0);
             }
-            // before the CTA may exit: the last load armed on each stage has landed
-            for (int s = 0; s < STAGES && s < i; ++s) {
-                const int last = i - 1 - ((i - 1 - s) % STAGES);
-                mbar_wait(&full[s], (uint32_t)((last / STAGES) & 1), status);
+            if (++s == STAGES) {
+                s = 0;
+                ph ^= 1;
             }
         }
+        // before the CTA may exit: the last load armed on each stage has landed
+        for (int s = 0; s < STAGES && s < i; ++s) {
+            const int last = i - 1 - ((i - 1 - s) % STAGES);
+            mbar_wait(&full[s], (uint32_t)((last / STAGES) & 1), status);
+        }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = f8_idesc(128, MT);
-            int i = 0;
-            for (; i < nkb; ++i) {
-                const int s = i % STAGES, b = i & 1;
-                // the first use of each accumulator waits for nothing (the phase before the first)
-                if (!mbar_wait(&acc_empty[b], (uint32_t)(((i >> 1) & 1) ^ 1), status)) break;
-                if (!mbar_wait(&full[s], (uint32_t)((i / STAGES) & 1), status)) break;
-                tc_fence_after();
+        constexpr uint32_t idesc = f8_idesc(128, MT);
+        const uint64_t w_desc = smem_desc(smem_u32(tile_w(0)), 16, 1024, 2), x_desc = smem_desc(smem_u32(tile_x(0)), 16, 1024, 2);
+        int i = 0;
+        for (int s = 0, ph = 0; i < nkb; ++i) {
+            const int b = i & 1;
+            // the first use of each accumulator waits for nothing (the phase before the first)
+            if (!f8_warp_wait(&acc_empty[b], (uint32_t)(((i >> 1) & 1) ^ 1), status)) break;
+            if (!f8_warp_wait(&full[s], (uint32_t)ph, status)) break;
+            tc_fence_after();
+            const uint64_t off = (uint64_t)(s * (Cfg::STAGE_BYTES >> 4));
+            if (f8_elect()) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    f8_mma(tmem + b * MT, smem_desc(smem_u32(tile_w(s)) + kk * 32, 16, 1024, 2),
-                           smem_desc(smem_u32(tile_x(s)) + kk * 32, 16, 1024, 2), idesc, kk ? 1u : 0u);
+                    f8_mma(tmem + b * MT, w_desc + off + 2 * kk, x_desc + off + 2 * kk, idesc, kk ? 1u : 0u);
                 tc_commit(&empty[s]);
                 tc_commit(&acc_full[b]);
             }
-            // before tensor memory is freed: every MMA issued has completed (bounded)
-            if (i) {
-                tc_commit(drain);
-                mbar_wait(drain, 0, status);
+            __syncwarp();
+            if (++s == STAGES) {
+                s = 0;
+                ph ^= 1;
             }
+        }
+        // before tensor memory is freed: every MMA issued has completed (bounded)
+        if (i) {
+            if (f8_elect()) tc_commit(drain);
+            __syncwarp();
+            mbar_wait(drain, 0, status);
         }
     } else if (warp < 4) {
         // factors of chunk c (K blocks kChunk c ..) for the tile's rows, rows past M zero
@@ -216,7 +262,7 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             for (int c0 = 0; c0 < COLS; c0 += 16) {
                 uint32_t d[16];
                 tmem_ld16(tm + b * MT + c0, d);
-                tmem_ld_wait();
+                tmem_ld_wait_for(d);
 #pragma unroll
                 for (int c = 0; c < 16; c += 4) {
                     const float4 s4 = *reinterpret_cast<const float4 *>(f + c0 + c);
@@ -271,6 +317,300 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, Cfg::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------- wide ----
+
+constexpr int kWStages = 6;
+constexpr int kWStageBytes = 2 * 128 * 128;                   // this CTA's 128 token rows and 128 weight rows
+constexpr int kWEpiWarps = 8;
+constexpr int kWPieceBytes = 32 * 64;                         // a promotion warp's 32 rows x 64 bytes of y
+constexpr int kWOutOff = kWStages * kWStageBytes;
+constexpr int kWFacOff = kWOutOff + kWEpiWarps * kWPieceBytes;
+constexpr int kWFacAhead = 8;                                 // K blocks whose factors are on their way
+constexpr int kWFacSlots = kWFacAhead + 4;
+constexpr int kWFacPitch = 132;                               // 128 token rows, the two weight blocks
+constexpr int kWBarOff = kWFacOff + kWFacSlots * kWFacPitch * 4;
+constexpr int kWSmem = kWBarOff + 256 + 1024;
+constexpr int kWThreads = 384;
+static_assert(kWSmem <= 232448, "shared memory of one CTA");
+
+__device__ __forceinline__ uint32_t f8_mapa(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+// Arrival on a barrier of a CTA of the pair (no generic-memory data goes with it).
+__device__ __forceinline__ void f8_arrive_at(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// The MMAs issued so far complete -> one arrival on `bar` in both CTAs of the pair.
+__device__ __forceinline__ void f8_commit_pair(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+                 : "memory");
+}
+__device__ __forceinline__ void f8_mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc));
+}
+// acc += f * d on 16 accumulator columns.
+__device__ __forceinline__ void f8_promote(float (&acc)[16], const uint32_t (&d)[16], float f) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) acc[j] = fmaf(__uint_as_float(d[j]), f, acc[j]);
+}
+
+template <bool OUT_BF16>
+__global__ void __launch_bounds__(kWThreads, 1)
+fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                     const float *__restrict__ as, const float *__restrict__ bs, int M, int N, int num_k,
+                     void *__restrict__ y, int *status) {
+    pdl_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kWBarOff);
+    uint64_t *full = bars, *empty = bars + kWStages;
+    uint64_t *acc_full = bars + 2 * kWStages, *acc_empty = acc_full + 4, *drain = acc_full + 8;   // [buffer][half]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 9);
+    auto tile_a = [&](int s) { return sm + s * kWStageBytes; };
+    auto tile_b = [&](int s) { return sm + s * kWStageBytes + 128 * 128; };
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int rank = (int)f8_cluster_rank();
+    const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
+    const int tiles_n = (N + 255) / 256;
+    const int num_tiles = tiles_n * ((M + 255) / 256);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kWStages; ++s) {
+            mbar_init(&full[s], rank == 0 ? 2 : 1);   // this CTA's TMA; in the leader also the peer's word that its own landed
+            mbar_init(&empty[s], 1);                  // the leader's commit
+        }
+        for (int b = 0; b < 4; ++b) {
+            mbar_init(&acc_full[b], 2);               // the leader's commit, and warp 3: the K block's factors
+            mbar_init(&acc_empty[b], kWEpiWarps);     // leader only: the half's promotion warps of both CTAs
+        }
+        mbar_init(drain, 1);
+        fence_barrier_init();
+        tma_prefetch_desc(&map_a);
+        tma_prefetch_desc(&map_b);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    f8_cluster_sync();   // both CTAs' barriers are initialised and tensor memory is allocated
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            int it = 0, s = 0;
+            uint32_t ph = 1;
+            bool ok = true;
+            for (int t = pair; t < num_tiles && ok; t += npairs) {
+                // of the weight rows: 64 of the tile's first 128 columns, 64 of its second
+                const int m0 = t / tiles_n * 256 + rank * 128, n0 = t % tiles_n * 256 + rank * 64;
+                for (int k = 0; k < num_k; ++k, ++it) {
+                    if (!(ok = f8_warp_wait(&empty[s], ph, status))) break;
+                    if (f8_elect()) {
+                        mbar_arrive_expect_tx(&full[s], kWStageBytes);
+                        tma_load_2d(tile_a(s), &map_a, &full[s], k * 128, m0);
+                        tma_load_2d(tile_b(s), &map_b, &full[s], k * 128, n0);
+                        tma_load_2d(tile_b(s) + 64 * 128, &map_b, &full[s], k * 128, n0 + 128);
+                    }
+                    if (++s == kWStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            // before the CTA may exit: the latest load armed on each stage has landed
+            for (int s = 0; s < kWStages && s < it; ++s) {
+                const int last = it - 1 - ((it - 1 - s) % kWStages);
+                mbar_wait(&full[s], (uint32_t)((last / kWStages) & 1), status);
+            }
+        } else if (warp == 1 && rank == 0) {
+            constexpr uint32_t idesc = f8_idesc(256, 128);
+            const uint64_t a_desc = smem_desc(smem_u32(tile_a(0)), 16, 1024, 2), b_desc = smem_desc(smem_u32(tile_b(0)), 16, 1024, 2);
+            const int total = (num_tiles - pair + npairs - 1) / npairs * num_k;   // K blocks of this pair's tiles
+            int it = 0, s = 0;
+            uint32_t ph = 0;
+            for (; it < total; ++it) {
+                if (!f8_warp_wait(&full[s], ph, status)) break;
+                const uint64_t off = (uint64_t)(s * (kWStageBytes >> 4));
+                bool ok = true;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int b = 2 * (it & 1) + h;
+                    if (!(ok = f8_warp_wait(&acc_empty[b], (uint32_t)(((it >> 1) & 1) ^ 1), status))) break;
+                    tc_fence_after();
+                    if (f8_elect()) {
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            f8_mma_pair(tmem + b * 128, a_desc + off + 2 * kk, b_desc + off + 2 * kk + h * (64 * 128 >> 4), idesc,
+                                        kk ? 1u : 0u);
+                        f8_commit_pair(&acc_full[b]);
+                        if (h == 1) f8_commit_pair(&empty[s]);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (++s == kWStages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            // before the pair may free tensor memory: every MMA issued has completed (bounded)
+            if (f8_elect()) f8_commit_pair(drain);
+            __syncwarp();
+            mbar_wait(drain, 0, status);
+        } else if (warp == 2 && lane == 0 && rank == 1) {
+            const uint32_t at = f8_mapa(full, 0);
+            int it = 0;
+            bool ok = true;
+            for (int t = pair; t < num_tiles && ok; t += npairs)
+                for (int k = 0; k < num_k && ok; ++k, ++it) {
+                    const int s = it % kWStages;
+                    ok = mbar_wait(&full[s], (uint32_t)((it / kWStages) & 1), status);
+                    if (ok) f8_arrive_at(at + (uint32_t)(s * 8));
+                }
+        } else if (warp == 3) {
+            // as[m, B] of the tile's rows and bs[n / 128, B] of its two weight blocks, eight K blocks ahead by
+            // asynchronous copies (a load that was waited for one block later took longer than the MMAs).
+            // K block `it` is handed over once the block two before it is in its accumulator: the MMAs of
+            // that one waited for the promotion of the one four before `it`, whose slot can be written again.
+            float *fac = reinterpret_cast<float *>(sm + kWFacOff);
+            const int rows_n = (N + 127) / 128;
+            const int total = (num_tiles - pair + npairs - 1) / npairs * num_k;
+            int pt = pair, pk = 0, pslot = 0;
+            const float *pa[4], *pb;
+            auto aim = [&] {   // at the rows of tile pt
+                const int tm = pt / tiles_n, m0 = tm * 256 + rank * 128 + lane, nb = (pt - tm * tiles_n) * 2;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) pa[j] = as + (int64_t)min(m0 + 32 * j, M - 1) * num_k;
+                pb = bs + (int64_t)min(nb + (lane & 1), rows_n - 1) * num_k;
+            };
+            aim();
+            auto fetch = [&](int i) {
+                if (i < total) {
+                    float *to = fac + pslot * kWFacPitch;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) cp_async4(to + 32 * j + lane, pa[j] + pk);
+                    if (lane < 2) cp_async4(to + 128 + lane, pb + pk);
+                    if (++pk == num_k && i + 1 < total) {
+                        pk = 0;
+                        pt += npairs;
+                        aim();
+                    }
+                    if (++pslot == kWFacSlots) pslot = 0;
+                }
+                cp_async_commit();
+            };
+            for (int i = 0; i < kWFacAhead; ++i) fetch(i);
+            for (int it = 0; it < total; ++it) {
+                const int b = 2 * (it & 1);
+                if (it >= 2) {
+                    const uint32_t ph = (uint32_t)(((it >> 1) & 1) ^ 1);
+                    if (!f8_warp_wait(&acc_full[b], ph, status) || !f8_warp_wait(&acc_full[b + 1], ph, status)) break;
+                }
+                fetch(it + kWFacAhead);
+                cp_async_wait<kWFacAhead>();
+                __syncwarp();
+                if (lane < 2) mbar_arrive(&acc_full[b + lane]);
+            }
+            cp_async_wait<0>();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
+        const uint32_t leader_empty = f8_mapa(&acc_empty[half], 0);
+        const int r0 = rank * 128 + quarter * 32;
+        uint8_t *piece = sm + kWOutOff + (warp - 4) * kWPieceBytes;
+        const float *fac = reinterpret_cast<const float *>(sm + kWFacOff);
+        int fslot = 0;
+        int it = 0;
+        bool ok = true;
+        for (int t = pair; t < num_tiles && ok; t += npairs) {
+            float acc[8][16];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[c][j] = 0.0f;
+            for (int k = 0; k < num_k; ++k, ++it) {
+                const int b = it & 1;
+                if (!(ok = f8_warp_wait(&acc_full[2 * b + half], (uint32_t)((it >> 1) & 1), status))) break;
+                tc_fence_after();
+                const float f = fac[fslot * kWFacPitch + quarter * 32 + lane] * fac[fslot * kWFacPitch + 128 + half];
+                if (++fslot == kWFacSlots) fslot = 0;
+                uint32_t d[2][16];   // sixteen columns are loaded while the sixteen before are added
+                tmem_ld16(tm + b * 256, d[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    tmem_ld_wait_for(d[c & 1]);
+                    if (c < 7) {
+                        tmem_ld16(tm + b * 256 + 16 * (c + 1), d[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) f8_arrive_at(leader_empty + (uint32_t)(b * 16));
+                    }
+                    f8_promote(acc[c], d[c & 1], f);
+                }
+            }
+            if (!ok) break;
+            // a row of y lies in one thread: pieces of 32 rows x 64 bytes turn in the warp's shared memory
+            // (16-byte chunk c of row r at chunk c ^ (r / 2 % 4): no bank conflicts either way) so that a store
+            // covers eight runs of 64 bytes instead of 32 of 16
+            constexpr int CPP = OUT_BF16 ? 32 : 16;      // columns per piece
+            const int m_base = t / tiles_n * 256 + r0, n_base = t % tiles_n * 256 + half * 128;
+#pragma unroll
+            for (int pc = 0; pc < 128 / CPP; ++pc) {
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float *v = OUT_BF16 ? &acc[2 * pc + c / 2][8 * (c % 2)] : &acc[pc][4 * c];
+                    uint4 u;
+                    if constexpr (OUT_BF16) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const __nv_bfloat162 p2 = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                            w[j] = *reinterpret_cast<const uint32_t *>(&p2);
+                        }
+                        u = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+                        u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+                    }
+                    *reinterpret_cast<uint4 *>(piece + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = u;
+                }
+                __syncwarp();
+                const int c = lane & 3, n = n_base + pc * CPP + c * (CPP / 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + lane / 4;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(piece + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
+                    if (m_base + r < M && n < N)
+                        *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(y) + ((int64_t)(m_base + r) * N + n) * (OUT_BF16 ? 2 : 4)) = u;
+                }
+            }
+        }
+    }
+
+    // neither CTA frees tensor memory or exits while the pair's MMAs, reads or arrivals may touch it
+    tc_fence_before();
+    f8_cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 
@@ -350,9 +690,48 @@ cudaError_t launch_narrow(const Fp8GemmArgs &g, cudaStream_t st) {
     return g.out_bf16 ? launch_narrow_t<MT, true>(g, st) : launch_narrow_t<MT, false>(g, st);
 }
 
+template <bool OUT_BF16>
+cudaError_t launch_wide(const Fp8GemmArgs &g, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeClusterDimension;
+    attrs[0].val.clusterDim.x = 2;
+    attrs[0].val.clusterDim.y = 1;
+    attrs[0].val.clusterDim.z = 1;
+    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(kWThreads);
+    cfg.dynamicSmemBytes = kWSmem;
+    cfg.stream = st;
+    cfg.attrs = attrs;
+    cfg.numAttrs = 2;
+    static PerDevice<int> max_pairs;   // as many pairs as run at once
+    int pairs = 0;
+    const cudaError_t e = max_pairs.get(
+        [&cfg](int, int &r) {
+            cudaError_t x = cudaFuncSetAttribute(fp8_gemm_wide_kernel<OUT_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
+            if (x != cudaSuccess) return x;
+            cudaLaunchConfig_t q = cfg;
+            q.gridDim = dim3(2);
+            int clusters = 0;
+            if ((x = cudaOccupancyMaxActiveClusters(&clusters, fp8_gemm_wide_kernel<OUT_BF16>, &q)) != cudaSuccess) return x;
+            r = clusters > 0 ? clusters : 1;
+            return cudaSuccess;
+        },
+        &pairs);
+    if (e != cudaSuccess) return e;
+    CUtensorMap ma, mb;
+    if (!f8_map(&ma, g.aq, (uint64_t)g.M, (uint64_t)g.K, 128) || !f8_map(&mb, g.bq, (uint64_t)g.N, (uint64_t)g.K, 64))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = (int64_t)((g.N + 255) / 256) * ((g.M + 255) / 256);
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_wide_kernel<OUT_BF16>, ma, mb, g.as, g.bs, g.M, g.N, (g.K + 127) / 128, g.y, g.status);
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st) {
+    if (g.M > 128) return g.out_bf16 ? launch_wide<true>(g, st) : launch_wide<false>(g, st);
     if (g.M <= 16) return launch_narrow<16>(g, st);
     if (g.M <= 32) return launch_narrow<32>(g, st);
     if (g.M <= 64) return launch_narrow<64>(g, st);
