@@ -518,117 +518,150 @@ def gdn_short_conv1d_silu_decode(x, weight, conv_state, parts=None, y=None, stre
 
 # ---------------------------------------------------- FP8 and pooled decode ----
 # These calls run on the device of their tensors, whichever device is current, and outputs that they
-# allocate belong to the stream that writes them.
+# allocate belong to the stream that writes them. They are made once per layer and token, where a call's
+# time on the host is longer than its kernel: each checks its tensors in one pass (_ok) and goes
+# through the named checks above only to say what is wrong.
 
 _F8, _BF = (torch.float8_e4m3fn,), (torch.bfloat16,)
+_f8, _bf, _f32, _i32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
 
 
-def _launch(name, device, stream, *args):
-    """The library call `name` on `stream` (default: the device's current stream)."""
+def _ok(dev, *checks) -> bool:
+    """Whether every (tensor, dtype, elements) is a contiguous tensor of that dtype on CUDA device `dev` with at
+    least that many elements."""
+    if dev < 0:
+        return False
+    for t, dtype, need in checks:
+        if t.dtype is not dtype or t.get_device() != dev or t.numel() < need or not t.is_contiguous():
+            return False
+    return True
+
+
+def _launch(fn, dev, stream, *args):
+    """The library call `fn` on `stream` (default: the device's current stream) with device `dev` current."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError("stream is on %s, the call's tensors on %s" % (stream.device, device))
-    if device.index == torch.cuda.current_device():
-        st = getattr(LIB, name)(*args, stream.cuda_stream)
+        raw = torch._C._cuda_getCurrentRawStream(dev)   # the current stream's handle, without a Stream object
+    elif stream.device.index != dev:
+        raise ValueError("stream is on %s, the call's tensors on cuda:%d" % (stream.device, dev))
     else:
-        with torch.cuda.device(device):
-            st = getattr(LIB, name)(*args, stream.cuda_stream)
+        raw = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
     if st != GDN_OK:
-        raise GdnError(name, st)
+        raise GdnError(fn.__name__, st)
 
 
-def _new(shape, dtype, device, stream, like=torch.empty):
+def _new(shape, dtype, dev, stream, like=torch.empty):
     if stream is None:
-        return like(shape, dtype=dtype, device=device)
+        return like(shape, dtype=dtype, device="cuda:%d" % dev)
     with torch.cuda.stream(stream):
-        return like(shape, dtype=dtype, device=device)
+        return like(shape, dtype=dtype, device="cuda:%d" % dev)
 
 
-def _rows2d(name, t):
+def _row_stride(name, t):
     """Row stride of a 2-D tensor whose rows may be strided (a column slice of a wider matrix)."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError("%s must be 2-D with unit column stride" % name)
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    return ld if rows > 1 else max(cols, 1)
 
 
-def _fp8_quantize(name, x, xq, xs, srows, stream):
-    ldx = _rows2d("x", x)
+def _fp8_quantize(fn, x, xq, xs, per_row, stream):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor")
+    ldx = _row_stride("x", x)
     M, K = x.shape
     kb = (K + 127) // 128
-    _args(x.device, x=(x, _IO, None), xq=(xq, _F8, M * K), xs=(xs, _F32, srows * kb))
-    _contig(xq, xs)
+    rows = M if per_row else (M + 127) // 128
+    dev = x.get_device()
+    dt = x.dtype
+    if (dev < 0 or not (dt is _bf or dt is _f32) or not (xq is None or _ok(dev, (xq, _f8, M * K)))
+            or not (xs is None or _ok(dev, (xs, _f32, rows * kb)))):
+        _args(x.device, x=(x, _IO, None), xq=(xq, _F8, M * K), xs=(xs, _F32, rows * kb))
+        _contig(xq, xs)
     if xq is None:
-        xq = _new((M, K), torch.float8_e4m3fn, x.device, stream)
+        xq = _new((M, K), _f8, dev, stream)
     if xs is None:
-        xs = _new((srows, kb), torch.float32, x.device, stream)
-    _launch(name, x.device, stream, x.data_ptr(), ldx, _dt(x), M, K, xq.data_ptr(), xs.data_ptr())
+        xs = _new((rows, kb), _f32, dev, stream)
+    _launch(fn, dev, stream, x.data_ptr(), ldx, GDN_BF16 if dt is _bf else GDN_F32, M, K, xq.data_ptr(), xs.data_ptr())
     return xq, xs
 
 
 def fp8_quantize_act(x, xq=None, xs=None, stream=None):
     """x [M, K] bf16/fp32 (rows may be strided) -> (xq [M, K] float8_e4m3fn, xs [M, ceil(K/128)] fp32),
     one scale per 128 values of a row. K % 16 == 0."""
-    return _fp8_quantize("fp8_quantize_act", x, xq, xs, x.shape[0], stream)
+    return _fp8_quantize(LIB.fp8_quantize_act, x, xq, xs, True, stream)
 
 
 def fp8_quantize_weight(w, wq=None, ws=None, stream=None):
     """w [N, K] bf16/fp32 (rows may be strided) -> (wq [N, K] float8_e4m3fn, ws [ceil(N/128), ceil(K/128)] fp32),
     one scale per 128 x 128 block. K % 16 == 0."""
-    return _fp8_quantize("fp8_quantize_weight", w, wq, ws, (w.shape[0] + 127) // 128, stream)
+    return _fp8_quantize(LIB.fp8_quantize_weight, w, wq, ws, False, stream)
 
 
 def fp8_gemm(aq, as_, bq, bs, out_dtype=torch.bfloat16, y=None, stream=None):
     """(aq [M, K], as [M, ceil(K/128)]) x (bq [N, K], bs [ceil(N/128), ceil(K/128)])^T -> y [M, N]."""
     M, K = aq.shape
-    N = bq.shape[0]
+    N, Kb = bq.shape
     kb = (K + 127) // 128
-    _args(aq.device, aq=(aq, _F8, None), as_=(as_, _F32, M * kb), bq=(bq, _F8, N * K),
-          bs=(bs, _F32, (N + 127) // 128 * kb), y=(y, _IO, M * N))
-    _contig(aq, as_, bq, bs, y)
-    if bq.shape[1] != K:
-        raise ValueError("bq has %d columns, aq %d" % (bq.shape[1], K))
+    dev = aq.get_device()
+    if not (_ok(dev, (aq, _f8, 0), (as_, _f32, M * kb), (bq, _f8, 0), (bs, _f32, (N + 127) // 128 * kb))
+            and (y is None or _ok(dev, (y, y.dtype, M * N)) and (y.dtype is _bf or y.dtype is _f32))):
+        _args(aq.device, aq=(aq, _F8, None), as_=(as_, _F32, M * kb), bq=(bq, _F8, None),
+              bs=(bs, _F32, (N + 127) // 128 * kb), y=(y, _IO, M * N))
+        _contig(aq, as_, bq, bs, y)
+    if Kb != K:
+        raise ValueError("bq has %d columns, aq %d" % (Kb, K))
     if y is None:
-        y = _new((M, N), out_dtype, aq.device, stream)
-    _launch("fp8_gemm", aq.device, stream, aq.data_ptr(), as_.data_ptr(), bq.data_ptr(), bs.data_ptr(), M, N, K, _dt(y),
-            y.data_ptr())
+        y = _new((M, N), out_dtype, dev, stream)
+    _launch(LIB.fp8_gemm, dev, stream, aq.data_ptr(), as_.data_ptr(), bq.data_ptr(), bs.data_ptr(), M, N, K, _dt(y), y.data_ptr())
     return y
 
 
 def gdn_gated_rmsnorm_silu_fp8(o, z, weight, eps: float = 1e-6, xq=None, xs=None, stream=None):
     """o, z [M, Hv, D] -> (xq [M, Hv * D] float8_e4m3fn, xs [M, ceil(Hv * D / 128)] fp32)."""
     M, Hv, D = o.shape
-    kb = (Hv * D + 127) // 128
-    _args(o.device, o=(o, _IO, None), z=(z, (o.dtype,), M * Hv * D), weight=(weight, _F32, D),
-          xq=(xq, _F8, M * Hv * D), xs=(xs, _F32, M * kb))
-    _contig(o, z, weight, xq, xs)
+    K = Hv * D
+    kb = (K + 127) // 128
+    dev, dt = o.get_device(), o.dtype
+    if not ((dt is _bf or dt is _f32) and _ok(dev, (o, dt, 0), (z, dt, M * K), (weight, _f32, D))
+            and (xq is None or _ok(dev, (xq, _f8, M * K))) and (xs is None or _ok(dev, (xs, _f32, M * kb)))):
+        _args(o.device, o=(o, _IO, None), z=(z, (dt,), M * K), weight=(weight, _F32, D), xq=(xq, _F8, M * K), xs=(xs, _F32, M * kb))
+        _contig(o, z, weight, xq, xs)
     if xq is None:
-        xq = _new((M, Hv * D), torch.float8_e4m3fn, o.device, stream)
+        xq = _new((M, K), _f8, dev, stream)
     if xs is None:
-        xs = _new((M, kb), torch.float32, o.device, stream)
-    _launch("gdn_gated_rmsnorm_silu_fp8", o.device, stream, o.data_ptr(), z.data_ptr(), weight.data_ptr(), eps, M, Hv, D,
-            _dt(o), xq.data_ptr(), xs.data_ptr())
+        xs = _new((M, kb), _f32, dev, stream)
+    _launch(LIB.gdn_gated_rmsnorm_silu_fp8, dev, stream, o.data_ptr(), z.data_ptr(), weight.data_ptr(), eps, M, Hv, D,
+            GDN_BF16 if dt is _bf else GDN_F32, xq.data_ptr(), xs.data_ptr())
     return xq, xs
 
 
-def _pooled_args(q, k, v, a, b, A_log, dt_bias, state_pool, slots, **more):
-    """Checks shared by the pooled decode calls; returns (B, Hk, Hv, D, gate row stride)."""
-    if any(t is None for t in (a, b, state_pool, slots)):
-        raise ValueError("a, b, state_pool and slots are required")
+def _pooled_sizes(q, k, v, a, b, A_log, dt_bias, state_pool, slots):
+    """Checks shared by the pooled decode calls; returns (device index, B, Hk, Hv, gate row stride)."""
     B, Hk, D = q.shape
     Hv = v.shape[1]
-    if state_pool.dim() != 4 or tuple(state_pool.shape[1:]) != (Hv, D, D):
+    if a is None or b is None or state_pool is None or slots is None:
+        raise ValueError("a, b, state_pool and slots are required")
+    if state_pool.shape[1:] != (Hv, D, D):
         raise ValueError("state_pool must be [num_slots, %d, %d, %d]" % (Hv, D, D))
-    if a.shape != (B, Hv) or b.shape != (B, Hv) or v.shape != (B, Hv, D) or k.shape != q.shape:
+    if a.shape != (B, Hv) or b.shape != a.shape or v.shape != (B, Hv, D) or k.shape != q.shape:
         raise ValueError("a, b must be [%d, %d], v [%d, %d, %d], k as q" % (B, Hv, B, Hv, D))
-    _args(q.device, q=(q, _BF, None), k=(k, _BF, None), v=(v, _BF, None), a=(a, _IO, None), b=(b, (a.dtype,), None),
-          A_log=(A_log, _F32, Hv), dt_bias=(dt_bias, _F32, Hv), state_pool=(state_pool, _F32, None),
-          slots=(slots, _I32, B), **more)
-    _contig(q, k, v, A_log, dt_bias, state_pool, slots)
-    ldg = _rows2d("a", a)
-    if _rows2d("b", b) != ldg:
+    dev, gt = q.get_device(), a.dtype
+    if not (_ok(dev, (q, _bf, 0), (k, _bf, 0), (v, _bf, 0), (A_log, _f32, Hv), (dt_bias, _f32, Hv), (state_pool, _f32, 0),
+                (slots, _i32, B)) and a.get_device() == dev and b.get_device() == dev and b.dtype is gt
+            and (gt is _bf or gt is _f32)):
+        _args(q.device, q=(q, _BF, None), k=(k, _BF, None), v=(v, _BF, None), a=(a, _IO, None), b=(b, (gt,), None),
+              A_log=(A_log, _F32, Hv), dt_bias=(dt_bias, _F32, Hv), state_pool=(state_pool, _F32, None), slots=(slots, _I32, B))
+        _contig(q, k, v, A_log, dt_bias, state_pool, slots)
+    ldg = _row_stride("a", a)
+    if _row_stride("b", b) != ldg:
         raise ValueError("a and b must have the same row stride")
-    return B, Hk, Hv, D, ldg
+    return dev, B, Hk, Hv, ldg
 
 
 def gdn_decode_step_pooled(q, k, v, a, b, A_log, dt_bias, state_pool, slots, scale: float = 1.0,
@@ -636,12 +669,15 @@ def gdn_decode_step_pooled(q, k, v, a, b, A_log, dt_bias, state_pool, slots, sca
     """gdn_decode_step on states in a pool: row i uses slot slots[i] (device int32 [B]) of state_pool
     [num_slots, Hv, 128, 128] fp32, in place; a negative slot marks a padded row, whose state and output
     stay as they are (a new output is zero there). a, b [B, Hv] bf16 or fp32, rows may be strided. Returns o."""
-    B, Hk, Hv, D, ldg = _pooled_args(q, k, v, a, b, A_log, dt_bias, state_pool, slots, o=(o, _IO, v.numel()))
-    _contig(o)
+    dev, B, Hk, Hv, ldg = _pooled_sizes(q, k, v, a, b, A_log, dt_bias, state_pool, slots)
+    D = q.shape[2]
     if o is None:
-        o = _new((B, Hv, D), out_dtype or q.dtype, q.device, stream, torch.zeros)
-    _launch("gdn_decode_step_pooled", q.device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(),
-            ldg, _dt(a), A_log.data_ptr(), dt_bias.data_ptr(), B, Hk, Hv, D, D, scale, int(bool(qk_l2norm)), GDN_BF16,
+        o = _new((B, Hv, D), out_dtype or q.dtype, dev, stream, torch.zeros)
+    elif not (_ok(dev, (o, o.dtype, v.numel())) and (o.dtype is _bf or o.dtype is _f32)):
+        _args(q.device, o=(o, _IO, v.numel()))
+        _contig(o)
+    _launch(LIB.gdn_decode_step_pooled, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), ldg,
+            _dt(a), A_log.data_ptr(), dt_bias.data_ptr(), B, Hk, Hv, D, D, scale, 1 if qk_l2norm else 0, GDN_BF16,
             state_pool.data_ptr(), state_pool.shape[0], slots.data_ptr(), o.data_ptr(), _dt(o))
     return o
 
@@ -652,23 +688,25 @@ def gdn_decode_step_pooled_gated_fp8(q, k, v, a, b, A_log, dt_bias, state_pool, 
     """gdn_decode_step_pooled with the gated RMSNorm and its FP8 encode fused: z [B, Hv, 128] bf16 (rows may
     be strided), norm_weight [128] fp32. Returns (xq [B, Hv*128] float8_e4m3fn, xs [B, Hv] fp32, o or None);
     o (bf16) is written only when given. New outputs are zero in padded rows."""
+    dev, B, Hk, Hv, ldg = _pooled_sizes(q, k, v, a, b, A_log, dt_bias, state_pool, slots)
     if z is None or norm_weight is None:
         raise ValueError("z and norm_weight are required")
-    n = v.numel()
-    B, Hk, Hv, D, ldg = _pooled_args(q, k, v, a, b, A_log, dt_bias, state_pool, slots, z=(z, _BF, None),
-                                     norm_weight=(norm_weight, _F32, 128), xq=(xq, _F8, n), xs=(xs, _F32, n // 128),
-                                     o=(o, _BF, n))
-    _contig(norm_weight, xq, xs, o)
-    if z.shape != v.shape or (z.stride(2), z.stride(1)) != (1, D) and (Hv > 1 or z.stride(2) != 1):
+    D, n = q.shape[2], v.numel()
+    if not (z.dtype is _bf and z.get_device() == dev and _ok(dev, (norm_weight, _f32, 128))
+            and (xq is None or _ok(dev, (xq, _f8, n))) and (xs is None or _ok(dev, (xs, _f32, n // 128)))
+            and (o is None or _ok(dev, (o, _bf, n)))):
+        _args(q.device, z=(z, _BF, None), norm_weight=(norm_weight, _F32, 128), xq=(xq, _F8, n), xs=(xs, _F32, n // 128), o=(o, _BF, n))
+        _contig(norm_weight, xq, xs, o)
+    sb, sh, sd = z.stride() if z.dim() == 3 else (0, 0, 0)
+    if z.shape != v.shape or sd != 1 or (Hv > 1 and sh != D):
         raise ValueError("z must be [%d, %d, %d] with contiguous heads" % (B, Hv, D))
-    ldz = z.stride(0) if B > 1 else Hv * D
     if xq is None:
-        xq = _new((B, Hv * D), torch.float8_e4m3fn, q.device, stream, torch.zeros)
+        xq = _new((B, Hv * D), _f8, dev, stream, torch.zeros)
     if xs is None:
-        xs = _new((B, Hv), torch.float32, q.device, stream, torch.zeros)
-    _launch("gdn_decode_step_pooled_gated_fp8", q.device, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(),
-            b.data_ptr(), ldg, _dt(a), A_log.data_ptr(), dt_bias.data_ptr(), B, Hk, Hv, D, D, scale, int(bool(qk_l2norm)),
-            GDN_BF16, state_pool.data_ptr(), state_pool.shape[0], slots.data_ptr(), z.data_ptr(), ldz,
+        xs = _new((B, Hv), _f32, dev, stream, torch.zeros)
+    _launch(LIB.gdn_decode_step_pooled_gated_fp8, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(),
+            ldg, _dt(a), A_log.data_ptr(), dt_bias.data_ptr(), B, Hk, Hv, D, D, scale, 1 if qk_l2norm else 0, GDN_BF16,
+            state_pool.data_ptr(), state_pool.shape[0], slots.data_ptr(), z.data_ptr(), sb if B > 1 else Hv * D,
             norm_weight.data_ptr(), eps, xq.data_ptr(), xs.data_ptr(), None if o is None else o.data_ptr())
     return xq, xs, o
 
@@ -680,19 +718,23 @@ def gdn_short_conv1d_silu_decode_pooled(x, weight, conv_pool, slots, parts=None,
     K = weight.shape[1]
     if conv_pool is None or slots is None:
         raise ValueError("conv_pool and slots are required")
-    if conv_pool.dim() != 3 or tuple(conv_pool.shape[1:]) != (K - 1, C) or weight.shape[0] != C:
+    if conv_pool.shape[1:] != (K - 1, C) or weight.shape[0] != C:
         raise ValueError("conv_pool must be [num_slots, %d, %d] and weight [%d, K]" % (K - 1, C, C))
-    _args(x.device, x=x, weight=(weight, _F32, None), conv_pool=(conv_pool, _BF, None), slots=(slots, _I32, B),
-          y=(y, _BF, B * C))
-    _contig(weight, conv_pool, slots, y)
+    dev = x.get_device()
+    if not _ok(dev, (weight, _f32, 0), (conv_pool, _bf, 0), (slots, _i32, B)) or not (y is None or _ok(dev, (y, _bf, B * C))):
+        _args(x.device, x=x, weight=(weight, _F32, None), conv_pool=(conv_pool, _BF, None), slots=(slots, _I32, B), y=(y, _BF, B * C))
+        _contig(weight, conv_pool, slots, y)
     if y is None:
-        y = _new((B, C) if parts is None else (B * C,), torch.bfloat16, x.device, stream, torch.zeros)
-    widths = [C] if parts is None else [int(p) for p in parts]
-    _launch("gdn_short_conv1d_silu_decode_pooled", x.device, stream, x.data_ptr(), ldx, weight.data_ptr(), B, C, K,
-            conv_pool.data_ptr(), conv_pool.shape[0], slots.data_ptr(), y.data_ptr(),
-            (ctypes.c_int32 * len(widths))(*widths), len(widths))
+        y = _new((B, C), _bf, dev, stream, torch.zeros)
     if parts is None:
-        return y.view(-1)[:B * C].view(B, C)
+        widths, n = None, 0
+    else:
+        n = len(parts)
+        widths = (ctypes.c_int32 * n)(*parts)
+    _launch(LIB.gdn_short_conv1d_silu_decode_pooled, dev, stream, x.data_ptr(), ldx, weight.data_ptr(), B, C, K,
+            conv_pool.data_ptr(), conv_pool.shape[0], slots.data_ptr(), y.data_ptr(), widths, n)
+    if parts is None:
+        return y if y.shape == (B, C) else y.view(-1)[:B * C].view(B, C)
     return _conv_planes(parts, B, C, y, x.device)[2]
 
 

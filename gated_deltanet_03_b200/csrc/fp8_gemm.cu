@@ -20,7 +20,7 @@
 // 32 KB of loads for 512 cycles of MMA (a 128 x 128 tile on one SM: 32 KB for 256, and loads are what
 // bounds it). Persistent; the two accumulators take all of tensor memory, so that the MMAs of one K block
 // run while the block before is scaled and added by the eight promotion warps, 128 fp32 sums a thread
-// (register split by setmaxnreg: 128 x 56 + 256 x 224 = 384 x 168, the launch's own total).
+// (register split by setmaxnreg: 128 x 72 + 256 x 216 = 384 x 168, the launch's own total).
 //   warp 0     TMA producer of this CTA's operands;   warp 1     (leader) MMA issue;
 //   warp 2     (peer) tells the leader that a stage's operands have landed here;
 //   warp 3     the factors as[m, B] bs[n / 128, B] of this CTA's rows, through shared memory;
@@ -102,6 +102,18 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[N]) {
 __device__ __forceinline__ bool f8_elect() {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+// Whether the phase with the given parity has completed, without waiting.
+__device__ __forceinline__ bool f8_done(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
     return ok != 0;
 }
 // The whole warp waits (bounded); false in every lane if any lane's wait ran out.
@@ -328,7 +340,7 @@ constexpr int kWEpiWarps = 8;
 constexpr int kWPieceBytes = 32 * 64;                         // a promotion warp's 32 rows x 64 bytes of y
 constexpr int kWOutOff = kWStages * kWStageBytes;
 constexpr int kWFacOff = kWOutOff + kWEpiWarps * kWPieceBytes;
-constexpr int kWFacAhead = 8;                                 // K blocks whose factors are on their way
+constexpr int kWFacAhead = 3;                                 // K blocks whose factors are on their way
 constexpr int kWFacSlots = kWFacAhead + 4;
 constexpr int kWFacPitch = 132;                               // 128 token rows, the two weight blocks
 constexpr int kWBarOff = kWFacOff + kWFacSlots * kWFacPitch * 4;
@@ -357,10 +369,11 @@ __device__ __forceinline__ void f8_mma_pair(uint32_t d, uint64_t a, uint64_t b, 
         "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
-// acc += f * d on 16 accumulator columns.
-__device__ __forceinline__ void f8_promote(float (&acc)[16], const uint32_t (&d)[16], float f) {
+// acc += f * d on 32 accumulator columns. (Scalar FMAs: as packed f32x2 ones they need the loaded columns in
+// aligned register pairs, and the moves and spills cost a fifth of the kernel's time.)
+__device__ __forceinline__ void f8_promote(float (&acc)[32], const uint32_t (&d)[32], float f) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) acc[j] = fmaf(__uint_as_float(d[j]), f, acc[j]);
+    for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(d[j]), f, acc[j]);
 }
 
 template <bool OUT_BF16>
@@ -373,8 +386,8 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kWBarOff);
     uint64_t *full = bars, *empty = bars + kWStages;
-    uint64_t *acc_full = bars + 2 * kWStages, *acc_empty = acc_full + 4, *drain = acc_full + 8;   // [buffer][half]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 9);
+    uint64_t *acc_full = bars + 2 * kWStages, *acc_empty = acc_full + 2, *drain = acc_full + 4;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 5);
     auto tile_a = [&](int s) { return sm + s * kWStageBytes; };
     auto tile_b = [&](int s) { return sm + s * kWStageBytes + 128 * 128; };
 
@@ -389,9 +402,9 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             mbar_init(&full[s], rank == 0 ? 2 : 1);   // this CTA's TMA; in the leader also the peer's word that its own landed
             mbar_init(&empty[s], 1);                  // the leader's commit
         }
-        for (int b = 0; b < 4; ++b) {
-            mbar_init(&acc_full[b], 2);               // the leader's commit, and warp 3: the K block's factors
-            mbar_init(&acc_empty[b], kWEpiWarps);     // leader only: the half's promotion warps of both CTAs
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 2);                 // the leader's commit, and warp 3: the K block's factors
+            mbar_init(&acc_empty[b], 2 * kWEpiWarps);   // leader only: every promotion warp of the pair
         }
         mbar_init(drain, 1);
         fence_barrier_init();
@@ -410,21 +423,19 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     pdl_wait();
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
             int it = 0, s = 0;
             uint32_t ph = 1;
             bool ok = true;
             for (int t = pair; t < num_tiles && ok; t += npairs) {
-                // of the weight rows: 64 of the tile's first 128 columns, 64 of its second
-                const int m0 = t / tiles_n * 256 + rank * 128, n0 = t % tiles_n * 256 + rank * 64;
+                const int m0 = t / tiles_n * 256 + rank * 128, n0 = t % tiles_n * 256 + rank * 128;
                 for (int k = 0; k < num_k; ++k, ++it) {
                     if (!(ok = f8_warp_wait(&empty[s], ph, status))) break;
                     if (f8_elect()) {
                         mbar_arrive_expect_tx(&full[s], kWStageBytes);
                         tma_load_2d(tile_a(s), &map_a, &full[s], k * 128, m0);
                         tma_load_2d(tile_b(s), &map_b, &full[s], k * 128, n0);
-                        tma_load_2d(tile_b(s) + 64 * 128, &map_b, &full[s], k * 128, n0 + 128);
                     }
                     if (++s == kWStages) {
                         s = 0;
@@ -438,31 +449,25 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 mbar_wait(&full[s], (uint32_t)((last / kWStages) & 1), status);
             }
         } else if (warp == 1 && rank == 0) {
-            constexpr uint32_t idesc = f8_idesc(256, 128);
+            constexpr uint32_t idesc = f8_idesc(256, 256);
             const uint64_t a_desc = smem_desc(smem_u32(tile_a(0)), 16, 1024, 2), b_desc = smem_desc(smem_u32(tile_b(0)), 16, 1024, 2);
             const int total = (num_tiles - pair + npairs - 1) / npairs * num_k;   // K blocks of this pair's tiles
             int it = 0, s = 0;
             uint32_t ph = 0;
             for (; it < total; ++it) {
+                const int b = it & 1;
                 if (!f8_warp_wait(&full[s], ph, status)) break;
-                const uint64_t off = (uint64_t)(s * (kWStageBytes >> 4));
-                bool ok = true;
+                if (!f8_warp_wait(&acc_empty[b], (uint32_t)(((it >> 1) & 1) ^ 1), status)) break;
+                tc_fence_after();
+                if (f8_elect()) {
+                    const uint64_t off = (uint64_t)(s * (kWStageBytes >> 4));
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int b = 2 * (it & 1) + h;
-                    if (!(ok = f8_warp_wait(&acc_empty[b], (uint32_t)(((it >> 1) & 1) ^ 1), status))) break;
-                    tc_fence_after();
-                    if (f8_elect()) {
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            f8_mma_pair(tmem + b * 128, a_desc + off + 2 * kk, b_desc + off + 2 * kk + h * (64 * 128 >> 4), idesc,
-                                        kk ? 1u : 0u);
-                        f8_commit_pair(&acc_full[b]);
-                        if (h == 1) f8_commit_pair(&empty[s]);
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < 4; ++kk)
+                        f8_mma_pair(tmem + b * 256, a_desc + off + 2 * kk, b_desc + off + 2 * kk, idesc, kk ? 1u : 0u);
+                    f8_commit_pair(&acc_full[b]);
+                    f8_commit_pair(&empty[s]);
                 }
-                if (!ok) break;
+                __syncwarp();
                 if (++s == kWStages) {
                     s = 0;
                     ph ^= 1;
@@ -483,7 +488,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                     if (ok) f8_arrive_at(at + (uint32_t)(s * 8));
                 }
         } else if (warp == 3) {
-            // as[m, B] of the tile's rows and bs[n / 128, B] of its two weight blocks, eight K blocks ahead by
+            // as[m, B] of the tile's rows and bs[n / 128, B] of its two weight blocks, three K blocks ahead by
             // asynchronous copies (a load that was waited for one block later took longer than the MMAs).
             // K block `it` is handed over once the block two before it is in its accumulator: the MMAs of
             // that one waited for the promotion of the one four before `it`, whose slot can be written again.
@@ -516,55 +521,66 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             };
             for (int i = 0; i < kWFacAhead; ++i) fetch(i);
             for (int it = 0; it < total; ++it) {
-                const int b = 2 * (it & 1);
-                if (it >= 2) {
-                    const uint32_t ph = (uint32_t)(((it >> 1) & 1) ^ 1);
-                    if (!f8_warp_wait(&acc_full[b], ph, status) || !f8_warp_wait(&acc_full[b + 1], ph, status)) break;
-                }
+                const int b = it & 1;
+                if (it >= 2 && !f8_warp_wait(&acc_full[b], (uint32_t)(((it >> 1) & 1) ^ 1), status)) break;
                 fetch(it + kWFacAhead);
                 cp_async_wait<kWFacAhead>();
                 __syncwarp();
-                if (lane < 2) mbar_arrive(&acc_full[b + lane]);
+                if (lane == 0) mbar_arrive(&acc_full[b]);
             }
             cp_async_wait<0>();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
-        const uint32_t leader_empty = f8_mapa(&acc_empty[half], 0);
+        const uint32_t leader_empty = f8_mapa(acc_empty, 0);
         const int r0 = rank * 128 + quarter * 32;
         uint8_t *piece = sm + kWOutOff + (warp - 4) * kWPieceBytes;
         const float *fac = reinterpret_cast<const float *>(sm + kWFacOff);
         int fslot = 0;
+        auto factor = [&] {   // of this thread's row and half, the next K block's
+            const float f = fac[fslot * kWFacPitch + quarter * 32 + lane] * fac[fslot * kWFacPitch + 128 + half];
+            if (++fslot == kWFacSlots) fslot = 0;
+            return f;
+        };
         int it = 0;
         bool ok = true;
         for (int t = pair; t < num_tiles && ok; t += npairs) {
-            float acc[8][16];
+            float acc[4][32];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[c][j] = 0.0f;
+                for (int j = 0; j < 32; ++j) acc[c][j] = 0.0f;
+            uint32_t d[2][32];   // 32 columns are loaded while the 32 before are added, also from one K block to the next
+            ok = f8_warp_wait(&acc_full[it & 1], (uint32_t)((it >> 1) & 1), status);
+            if (!ok) break;
+            tc_fence_after();
+            tmem_ld32(tm + (it & 1) * 256, d[0]);
+            float f = factor();
             for (int k = 0; k < num_k; ++k, ++it) {
                 const int b = it & 1;
-                if (!(ok = f8_warp_wait(&acc_full[2 * b + half], (uint32_t)((it >> 1) & 1), status))) break;
-                tc_fence_after();
-                const float f = fac[fslot * kWFacPitch + quarter * 32 + lane] * fac[fslot * kWFacPitch + 128 + half];
-                if (++fslot == kWFacSlots) fslot = 0;
-                uint32_t d[2][16];   // sixteen columns are loaded while the sixteen before are added
-                tmem_ld16(tm + b * 256, d[0]);
+                const uint32_t next_ph = (uint32_t)(((it + 1) >> 1) & 1);
+                bool next = false;   // whether the next K block's accumulator is there, looked at early
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < 3; ++c) {
                     tmem_ld_wait_for(d[c & 1]);
-                    if (c < 7) {
-                        tmem_ld16(tm + b * 256 + 16 * (c + 1), d[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) f8_arrive_at(leader_empty + (uint32_t)(b * 16));
-                    }
+                    tmem_ld32(tm + b * 256 + 32 * (c + 1), d[(c + 1) & 1]);
+                    if (c == 1) next = f8_done(&acc_full[b ^ 1], next_ph);
                     f8_promote(acc[c], d[c & 1], f);
                 }
+                tmem_ld_wait_for(d[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) f8_arrive_at(leader_empty + (uint32_t)(b * 8));
+                const float f3 = f;
+                if (k + 1 < num_k) {
+                    if (!__all_sync(0xffffffffu, next) && !(ok = f8_warp_wait(&acc_full[b ^ 1], next_ph, status))) break;
+                    tc_fence_after();
+                    tmem_ld32(tm + (b ^ 1) * 256, d[0]);
+                    f = factor();
+                }
+                f8_promote(acc[3], d[1], f3);
             }
             if (!ok) break;
             // a row of y lies in one thread: pieces of 32 rows x 64 bytes turn in the warp's shared memory
@@ -577,7 +593,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float *v = OUT_BF16 ? &acc[2 * pc + c / 2][8 * (c % 2)] : &acc[pc][4 * c];
+                    const float *v = OUT_BF16 ? &acc[pc][8 * c] : &acc[pc / 2][16 * (pc % 2) + 4 * c];
                     uint4 u;
                     if constexpr (OUT_BF16) {
                         uint32_t w[4];
@@ -721,7 +737,7 @@ cudaError_t launch_wide(const Fp8GemmArgs &g, cudaStream_t st) {
         &pairs);
     if (e != cudaSuccess) return e;
     CUtensorMap ma, mb;
-    if (!f8_map(&ma, g.aq, (uint64_t)g.M, (uint64_t)g.K, 128) || !f8_map(&mb, g.bq, (uint64_t)g.N, (uint64_t)g.K, 64))
+    if (!f8_map(&ma, g.aq, (uint64_t)g.M, (uint64_t)g.K, 128) || !f8_map(&mb, g.bq, (uint64_t)g.N, (uint64_t)g.K, 128))
         return cudaErrorInvalidValue;
     const int64_t tiles = (int64_t)((g.N + 255) / 256) * ((g.M + 255) / 256);
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
