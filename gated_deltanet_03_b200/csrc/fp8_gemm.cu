@@ -8,12 +8,12 @@
 // fp8_gemm_narrow_kernel: the weight takes the MMA's M side (a tile of 128 rows of b on the 128 tensor-memory
 // lanes), MT activation rows (16, 32, 64 or 128) the N side, so that few tokens cost no more MMA or
 // tensor-memory work than they need. K is split over a cluster of CTAs along grid z where the tiles
-// alone would leave SMs idle; the partial sums meet in shared memory, summed in rank order.
+// alone would leave SMs idle; the partial sums are written into the shared memory of the CTA that stores them, which adds them in rank order.
 //   warp 0     TMA producer: weight tile (128 rows x 128 B) and activation tile (MT x 128 B) per K block;
 //   warp 1     tensor memory and the MMA issue (one thread);
-//   warps 2-3  the factors as[m, B] bs[n0 / 128, B] of the tile's MT rows, sixteen K blocks at a time;
-//   warps 4-   one weight row per thread (two threads for MT = 128, half the columns each): accumulator
-//              -> registers, one FMA per value, and at the end the tile through shared memory to y.
+//   warps 2-3  the factors as[m, B] bs[n0 / 128, B] of the tile's MT rows, eight K blocks at a time;
+//   warps 4-   one weight row and 32 of the MT columns per thread (16 for MT = 16): accumulator -> registers, one
+//              FMA per value, and at the end the tile through shared memory to y.
 //
 // fp8_gemm_wide_kernel, for many tokens: SM pairs (tcgen05.mma.cta_group::2) on 256 x 256 tiles, tokens on the M
 // side, CTA r of a pair holding 128 token rows and half of the 256 weight rows, so that a K block costs each SM
@@ -34,25 +34,29 @@
 namespace gdn {
 namespace {
 
-constexpr int kChunk = 16;                 // K blocks per set of staged factors
+constexpr int kChunk = 8;                  // K blocks per set of staged factors
+constexpr int kMaxSplit = 8;
 
 template <int MT>
 struct NarrowCfg {
-    static constexpr int STAGES = MT == 16 ? 6 : MT == 32 ? 5 : MT == 64 ? 4 : 6;
-    static constexpr int CTAS = MT == 128 ? 1 : 2;             // per SM
+    // Two CTAs an SM for the narrow tiles, whose K splits then reach further: 1 x 2048 x 4096 takes 4.8 us in eight
+    // ranges, 5.1 in four with one CTA an SM and twice the stages.
+    static constexpr int CTAS = MT <= 32 ? 2 : 1;
+    static constexpr int STAGES = MT == 16 ? 6 : MT == 32 ? 5 : MT == 64 ? 9 : 6;
     static constexpr int W_BYTES = 128 * 128, X_BYTES = MT * 128;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr int EPI_WARPS = MT == 128 ? 8 : 4;
-    static constexpr int COLS = MT == 128 ? 64 : MT;           // accumulator columns per thread
+    static constexpr int COLS = MT == 16 ? 16 : 32;            // accumulator columns per thread, one tensor-memory load
+    static constexpr int EPI_WARPS = 4 * MT / COLS;
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-    static constexpr int PITCH = 132;                          // fp32 pitch of a column of the partial tile
+    static constexpr int PITCH = 132;                          // fp32 pitch of a column of the partial sums
     static constexpr int OFF_SCL = STAGES * STAGE_BYTES;
     static constexpr int OFF_BAR = OFF_SCL + 2 * kChunk * MT * 4;
-    static constexpr int SMEM = OFF_BAR + 256 + 1024;
+    static constexpr int SMEM = OFF_BAR + 512 + 1024;
     static constexpr int TMEM_COLS = 2 * MT;
-    static_assert(MT * PITCH * 4 <= STAGES * STAGE_BYTES, "the partial tile fits over the stage ring");
+    static_assert(MT * PITCH * 4 <= STAGES * STAGE_BYTES, "the partial sums fit over the stage ring");
     static_assert(STAGE_BYTES % 1024 == 0, "stage bases stay 1024-byte aligned");
-    static_assert(CTAS * (SMEM + 1024) <= 233472, "CTAs per SM");
+    static_assert(MT % kMaxSplit == 0, "whole columns for every CTA of a cluster");
+    static_assert(SMEM <= 232448 && CTAS * (SMEM + 1024) <= 233472 && 8 * (2 * STAGES + 9) + 4 <= 512, "layout");
 };
 
 __device__ __forceinline__ uint32_t f8_cluster_rank() {
@@ -60,19 +64,20 @@ __device__ __forceinline__ uint32_t f8_cluster_rank() {
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
+__device__ __forceinline__ void f8_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void f8_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void f8_cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    f8_cluster_arrive();
+    f8_cluster_wait();
 }
-// 16 bytes at this CTA's shared address `p` as seen in CTA `rank` of the cluster.
-__device__ __forceinline__ float4 f8_ld_cluster(const void *p, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
+// The shared::cluster address of this CTA's object `p` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t f8_mapa(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void f8_st_cluster(uint32_t at, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
 }
 __device__ __forceinline__ void f8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -96,6 +101,9 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[N]) {
                           "+r"(r[i + 12]), "+r"(r[i + 13]), "+r"(r[i + 14]), "+r"(r[i + 15]));
 }
 
+__device__ __forceinline__ void f8_tmem_ld(uint32_t at, uint32_t (&d)[16]) { tmem_ld16(at, d); }
+__device__ __forceinline__ void f8_tmem_ld(uint32_t at, uint32_t (&d)[32]) { tmem_ld32(at, d); }
+
 // One lane of a whole warp. The warps that issue copies and MMAs run their loops with all lanes, the wait
 // included, and elect a lane around the instructions alone: the operands of those instructions are warp-uniform
 // registers, and from inside a one-lane branch each MMA took about 90 cycles to issue, more than it ran.
@@ -104,20 +112,10 @@ __device__ __forceinline__ bool f8_elect() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
     return ok != 0;
 }
-// Whether the phase with the given parity has completed, without waiting.
-__device__ __forceinline__ bool f8_done(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// The whole warp waits (bounded); false in every lane if any lane's wait ran out.
+// The whole warp waits (bounded); false in every lane if any lane's wait ran out. The first look is apart from
+// the bounded loop: with it a wait for a phase that is over takes 60 cycles, through the loop's code 120.
 __device__ __forceinline__ bool f8_warp_wait(uint64_t *bar, uint32_t parity, int *status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
@@ -181,6 +179,8 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
+    float acc[COLS];          // warps 4-: the scaled sums of this thread's weight row
+    bool acc_ok = false;
 
     if (warp == 0) {
         int i = 0;
@@ -254,76 +254,75 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             if (lane == 0) mbar_arrive(&scl_full[b]);
         }
     } else {
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + half * COLS;
-        float acc[COLS];
+        const int quarter = warp & 3, group = (warp - 4) >> 2;
+        const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + group * COLS;
 #pragma unroll
         for (int c = 0; c < COLS; ++c) acc[c] = 0.0f;
         bool ok = true;
         for (int i = 0; i < nkb; ++i) {
             const int b = i & 1, ch = i / kChunk;
-            if (lane == 0) {
-                ok = i % kChunk || mbar_wait(&scl_full[ch & 1], (uint32_t)((ch >> 1) & 1), status);
-                ok = ok && mbar_wait(&acc_full[b], (uint32_t)((i >> 1) & 1), status);
-            }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
+            ok = i % kChunk || f8_warp_wait(&scl_full[ch & 1], (uint32_t)((ch >> 1) & 1), status);
+            if (!ok || !(ok = f8_warp_wait(&acc_full[b], (uint32_t)((i >> 1) & 1), status))) break;
             tc_fence_after();
-            const float *f = scl + ((ch & 1) * kChunk + i % kChunk) * MT + half * COLS;
-#pragma unroll
-            for (int c0 = 0; c0 < COLS; c0 += 16) {
-                uint32_t d[16];
-                tmem_ld16(tm + b * MT + c0, d);
-                tmem_ld_wait_for(d);
-#pragma unroll
-                for (int c = 0; c < 16; c += 4) {
-                    const float4 s4 = *reinterpret_cast<const float4 *>(f + c0 + c);
-                    acc[c0 + c] = fmaf(__uint_as_float(d[c]), s4.x, acc[c0 + c]);
-                    acc[c0 + c + 1] = fmaf(__uint_as_float(d[c + 1]), s4.y, acc[c0 + c + 1]);
-                    acc[c0 + c + 2] = fmaf(__uint_as_float(d[c + 2]), s4.z, acc[c0 + c + 2]);
-                    acc[c0 + c + 3] = fmaf(__uint_as_float(d[c + 3]), s4.w, acc[c0 + c + 3]);
-                }
-            }
+            uint32_t d[COLS];
+            f8_tmem_ld(tm + b * MT, d);
+            const float4 *f4 = reinterpret_cast<const float4 *>(scl + ((ch & 1) * kChunk + i % kChunk) * MT + group * COLS);
+            tmem_ld_wait_for(d);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&acc_empty[b]);
-                if (i % kChunk == kChunk - 1) mbar_arrive(&scl_empty[ch & 1]);
-            }
-        }
-        // the tile into shared memory over the idle stage ring (every load was read by an MMA that has
-        // completed): column c (an activation row) at c * PITCH, weight rows consecutive
-        if (ok) {
-            float *part = reinterpret_cast<float *>(sm) + quarter * 32 + lane;
+            if (lane == 0) mbar_arrive(&acc_empty[b]);
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) part[(half * COLS + c) * Cfg::PITCH] = acc[c];
+            for (int c = 0; c < COLS / 4; ++c) {
+                const float4 f = f4[c];
+                acc[4 * c] = fmaf(__uint_as_float(d[4 * c]), f.x, acc[4 * c]);
+                acc[4 * c + 1] = fmaf(__uint_as_float(d[4 * c + 1]), f.y, acc[4 * c + 1]);
+                acc[4 * c + 2] = fmaf(__uint_as_float(d[4 * c + 2]), f.z, acc[4 * c + 2]);
+                acc[4 * c + 3] = fmaf(__uint_as_float(d[4 * c + 3]), f.w, acc[4 * c + 3]);
+            }
+            __syncwarp();
+            if (i % kChunk == kChunk - 1 && lane == 0) mbar_arrive(&scl_empty[ch & 1]);
         }
+        acc_ok = ok;
     }
-    // All threads reach the barriers, on the failure path too (the partial tile is then stale and the
-    // status word already says so). CTA r of a cluster stores the r-th share of the activation rows.
+    // Every thread reaches the barriers, on the failure path too (the sums are then stale and the status word
+    // already says so). At the first one every CTA's stage ring is idle (its loads have landed and been read by
+    // MMAs that have completed); then the sums of column c (an activation row) go over the ring of CTA c / cpr,
+    // into its rows of this CTA's; after the second nothing is written to or read from another CTA.
+    __syncwarp();
     if (split > 1) f8_cluster_sync();
     else __syncthreads();
-    const int c_lo = crank * MT / split, c_hi = (crank + 1) * MT / split;
-    for (int u = tid; u < (c_hi - c_lo) * 32; u += Cfg::THREADS) {
-        const int c = c_lo + u / 32, j = 4 * (u % 32);
-        const float *src = reinterpret_cast<const float *>(sm) + c * Cfg::PITCH + j;
-        if (m0 + c >= M || n0 + j >= N) continue;
-        float4 v;
+    const int cpr = MT / split;
+    if (acc_ok) {
+        const int quarter = warp & 3, group = (warp - 4) >> 2;
         if (split == 1) {
-            v = *reinterpret_cast<const float4 *>(src);
+            float *part = reinterpret_cast<float *>(sm) + quarter * 32 + lane;
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) part[(group * COLS + c) * Cfg::PITCH] = acc[c];
         } else {
-            v = f8_ld_cluster(src, 0);
-            for (int z = 1; z < split; ++z) {
-                const float4 t = f8_ld_cluster(src, (uint32_t)z);
-                v.x += t.x;
-                v.y += t.y;
-                v.z += t.z;
-                v.w += t.w;
+#pragma unroll
+            for (int c = 0; c < COLS; ++c) {
+                const int col = group * COLS + c, to = col / cpr;
+                const float *part = reinterpret_cast<const float *>(sm) + (crank * cpr + col - to * cpr) * Cfg::PITCH;
+                f8_st_cluster(f8_mapa(part + quarter * 32 + lane, (uint32_t)to), acc[c]);
             }
+        }
+    }
+    if (split > 1) f8_cluster_sync();
+    else __syncthreads();
+    for (int u = tid; u < cpr * 32; u += Cfg::THREADS) {
+        const int c = crank * cpr + u / 32, j = 4 * (u % 32);
+        if (m0 + c >= M || n0 + j >= N) continue;
+        const float *src = reinterpret_cast<const float *>(sm) + (u / 32) * Cfg::PITCH + j;
+        float4 v = *reinterpret_cast<const float4 *>(src);
+        for (int z = 1; z < split; ++z) {   // in rank order
+            const float4 t = *reinterpret_cast<const float4 *>(src + z * cpr * Cfg::PITCH);
+            v.x += t.x;
+            v.y += t.y;
+            v.z += t.z;
+            v.w += t.w;
         }
         store_y4<OUT_BF16>(y, (int64_t)(m0 + c) * N + n0 + j, v);
     }
-    if (split > 1) f8_cluster_sync();   // no CTA leaves before its partial tile has been read
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -334,25 +333,29 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
 
 // ------------------------------------------------------------------- wide ----
 
-constexpr int kWStages = 6;
-constexpr int kWStageBytes = 2 * 128 * 128;                   // this CTA's 128 token rows and 128 weight rows
-constexpr int kWEpiWarps = 8;
-constexpr int kWPieceBytes = 32 * 64;                         // a promotion warp's 32 rows x 64 bytes of y
-constexpr int kWOutOff = kWStages * kWStageBytes;
-constexpr int kWFacOff = kWOutOff + kWEpiWarps * kWPieceBytes;
-constexpr int kWFacAhead = 3;                                 // K blocks whose factors are on their way
-constexpr int kWFacSlots = kWFacAhead + 4;
-constexpr int kWFacPitch = 132;                               // 128 token rows, the two weight blocks
-constexpr int kWBarOff = kWFacOff + kWFacSlots * kWFacPitch * 4;
-constexpr int kWSmem = kWBarOff + 256 + 1024;
-constexpr int kWThreads = 384;
-static_assert(kWSmem <= 232448, "shared memory of one CTA");
+constexpr int kWFacAhead = 3;                 // K blocks whose factors are on their way
+constexpr int kWFacPitch = 132;               // 128 token rows, the four 64-column groups
+constexpr int kWPieceBytes = 32 * 64;         // a promotion warp's 32 rows x 64 bytes of y
 
-__device__ __forceinline__ uint32_t f8_mapa(const void *p, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-    return r;
-}
+template <int BN>
+struct WideCfg {
+    static constexpr int GROUPS = BN / 64;                        // column groups, a warpgroup of promotion warps each
+    static constexpr int WARPS = 4 * GROUPS;
+    static constexpr int THREADS = 128 + 32 * WARPS;
+    static constexpr int BUFS = BN == 128 ? 4 : 2;                // accumulators in tensor memory
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = BN == 256 ? 5 : BN == 192 ? 6 : 8;
+    static constexpr int FAC_SLOTS = kWFacAhead + 2 * BUFS;
+    static constexpr int OFF_OUT = STAGES * STAGE_BYTES;
+    static constexpr int OFF_FAC = OFF_OUT + WARPS * kWPieceBytes;
+    static constexpr int OFF_BAR = OFF_FAC + FAC_SLOTS * kWFacPitch * 4;
+    static constexpr int SMEM = OFF_BAR + 256 + 1024;
+    static constexpr bool SPLIT_REGS = BN == 256;
+    static constexpr int CH = BN == 256 ? 16 : 32;                // columns of a tensor-memory load
+    static_assert(STAGE_BYTES % 1024 == 0 && SMEM <= 232448 && BUFS * BN <= 512 && OFF_FAC % 16 == 0, "layout");
+};
+
 // Arrival on a barrier of a CTA of the pair (no generic-memory data goes with it).
 __device__ __forceinline__ void f8_arrive_at(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
@@ -369,42 +372,46 @@ __device__ __forceinline__ void f8_mma_pair(uint32_t d, uint64_t a, uint64_t b, 
         "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
-// acc += f * d on 32 accumulator columns. (Scalar FMAs: as packed f32x2 ones they need the loaded columns in
+// acc += f * d on CH accumulator columns. (Scalar FMAs: as packed f32x2 ones they need the loaded columns in
 // aligned register pairs, and the moves and spills cost a fifth of the kernel's time.)
-__device__ __forceinline__ void f8_promote(float (&acc)[32], const uint32_t (&d)[32], float f) {
+template <int CH>
+__device__ __forceinline__ void f8_promote(float *acc, const uint32_t (&d)[CH], float f) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) acc[j] = fmaf(__uint_as_float(d[j]), f, acc[j]);
+    for (int j = 0; j < CH; ++j) acc[j] = fmaf(__uint_as_float(d[j]), f, acc[j]);
 }
 
-template <bool OUT_BF16>
-__global__ void __launch_bounds__(kWThreads, 1)
+template <int BN, bool OUT_BF16>
+__global__ void __launch_bounds__(WideCfg<BN>::THREADS, 1)
 fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                      const float *__restrict__ as, const float *__restrict__ bs, int M, int N, int num_k,
                      void *__restrict__ y, int *status) {
+    using Cfg = WideCfg<BN>;
+    constexpr int STAGES = Cfg::STAGES, BUFS = Cfg::BUFS;
     pdl_launch_dependents();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kWBarOff);
-    uint64_t *full = bars, *empty = bars + kWStages;
-    uint64_t *acc_full = bars + 2 * kWStages, *acc_empty = acc_full + 2, *drain = acc_full + 4;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 5);
-    auto tile_a = [&](int s) { return sm + s * kWStageBytes; };
-    auto tile_b = [&](int s) { return sm + s * kWStageBytes + 128 * 128; };
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Cfg::OFF_BAR);
+    uint64_t *full = bars, *empty = bars + STAGES;
+    uint64_t *acc_full = bars + 2 * STAGES, *acc_empty = acc_full + BUFS, *drain = acc_empty + BUFS;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    auto tile_a = [&](int s) { return sm + s * Cfg::STAGE_BYTES; };
+    auto tile_b = [&](int s) { return sm + s * Cfg::STAGE_BYTES + Cfg::A_BYTES; };
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int rank = (int)f8_cluster_rank();
     const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
-    const int tiles_n = (N + 255) / 256;
+    const int tiles_n = (N + BN - 1) / BN;
     const int num_tiles = tiles_n * ((M + 255) / 256);
+    const int total = (num_tiles - pair + npairs - 1) / npairs * num_k;   // K blocks of this pair's tiles
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kWStages; ++s) {
+        for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], rank == 0 ? 2 : 1);   // this CTA's TMA; in the leader also the peer's word that its own landed
             mbar_init(&empty[s], 1);                  // the leader's commit
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < BUFS; ++b) {
             mbar_init(&acc_full[b], 2);                 // the leader's commit, and warp 3: the K block's factors
-            mbar_init(&acc_empty[b], 2 * kWEpiWarps);   // leader only: every promotion warp of the pair
+            mbar_init(&acc_empty[b], 2 * Cfg::WARPS);   // leader only: every promotion warp of the pair
         }
         mbar_init(drain, 1);
         fence_barrier_init();
@@ -423,54 +430,55 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     pdl_wait();
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 0) {
             int it = 0, s = 0;
             uint32_t ph = 1;
             bool ok = true;
             for (int t = pair; t < num_tiles && ok; t += npairs) {
-                const int m0 = t / tiles_n * 256 + rank * 128, n0 = t % tiles_n * 256 + rank * 128;
+                const int m0 = t / tiles_n * 256 + rank * 128, n0 = t % tiles_n * BN + rank * (BN / 2);
                 for (int k = 0; k < num_k; ++k, ++it) {
                     if (!(ok = f8_warp_wait(&empty[s], ph, status))) break;
                     if (f8_elect()) {
-                        mbar_arrive_expect_tx(&full[s], kWStageBytes);
+                        mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
                         tma_load_2d(tile_a(s), &map_a, &full[s], k * 128, m0);
                         tma_load_2d(tile_b(s), &map_b, &full[s], k * 128, n0);
                     }
-                    if (++s == kWStages) {
+                    if (++s == STAGES) {
                         s = 0;
                         ph ^= 1;
                     }
                 }
             }
             // before the CTA may exit: the latest load armed on each stage has landed
-            for (int s = 0; s < kWStages && s < it; ++s) {
-                const int last = it - 1 - ((it - 1 - s) % kWStages);
-                mbar_wait(&full[s], (uint32_t)((last / kWStages) & 1), status);
+            for (int s = 0; s < STAGES && s < it; ++s) {
+                const int last = it - 1 - ((it - 1 - s) % STAGES);
+                mbar_wait(&full[s], (uint32_t)((last / STAGES) & 1), status);
             }
         } else if (warp == 1 && rank == 0) {
-            constexpr uint32_t idesc = f8_idesc(256, 256);
+            constexpr uint32_t idesc = f8_idesc(256, BN);
             const uint64_t a_desc = smem_desc(smem_u32(tile_a(0)), 16, 1024, 2), b_desc = smem_desc(smem_u32(tile_b(0)), 16, 1024, 2);
-            const int total = (num_tiles - pair + npairs - 1) / npairs * num_k;   // K blocks of this pair's tiles
-            int it = 0, s = 0;
-            uint32_t ph = 0;
-            for (; it < total; ++it) {
-                const int b = it & 1;
-                if (!f8_warp_wait(&full[s], ph, status)) break;
-                if (!f8_warp_wait(&acc_empty[b], (uint32_t)(((it >> 1) & 1) ^ 1), status)) break;
+            int s = 0, b = 0;
+            uint32_t ph = 0, bph = 1;   // the first use of each accumulator waits for nothing
+            for (int it = 0; it < total; ++it) {
+                if (!f8_warp_wait(&full[s], ph, status) || !f8_warp_wait(&acc_empty[b], bph, status)) break;
                 tc_fence_after();
                 if (f8_elect()) {
-                    const uint64_t off = (uint64_t)(s * (kWStageBytes >> 4));
+                    const uint64_t off = (uint64_t)(s * (Cfg::STAGE_BYTES >> 4));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        f8_mma_pair(tmem + b * 256, a_desc + off + 2 * kk, b_desc + off + 2 * kk, idesc, kk ? 1u : 0u);
+                        f8_mma_pair(tmem + b * BN, a_desc + off + 2 * kk, b_desc + off + 2 * kk, idesc, kk ? 1u : 0u);
                     f8_commit_pair(&acc_full[b]);
                     f8_commit_pair(&empty[s]);
                 }
                 __syncwarp();
-                if (++s == kWStages) {
+                if (++s == STAGES) {
                     s = 0;
                     ph ^= 1;
+                }
+                if (++b == BUFS) {
+                    b = 0;
+                    bph ^= 1;
                 }
             }
             // before the pair may free tensor memory: every MMA issued has completed (bounded)
@@ -479,29 +487,30 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             mbar_wait(drain, 0, status);
         } else if (warp == 2 && lane == 0 && rank == 1) {
             const uint32_t at = f8_mapa(full, 0);
-            int it = 0;
-            bool ok = true;
-            for (int t = pair; t < num_tiles && ok; t += npairs)
-                for (int k = 0; k < num_k && ok; ++k, ++it) {
-                    const int s = it % kWStages;
-                    ok = mbar_wait(&full[s], (uint32_t)((it / kWStages) & 1), status);
-                    if (ok) f8_arrive_at(at + (uint32_t)(s * 8));
+            int s = 0;
+            uint32_t ph = 0;
+            for (int it = 0; it < total; ++it) {
+                if (!mbar_wait(&full[s], ph, status)) break;
+                f8_arrive_at(at + (uint32_t)(s * 8));
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1;
                 }
+            }
         } else if (warp == 3) {
-            // as[m, B] of the tile's rows and bs[n / 128, B] of its two weight blocks, three K blocks ahead by
+            // as[m, B] of the tile's rows and bs[n / 128, B] of its 64-column groups, some K blocks ahead by
             // asynchronous copies (a load that was waited for one block later took longer than the MMAs).
-            // K block `it` is handed over once the block two before it is in its accumulator: the MMAs of
-            // that one waited for the promotion of the one four before `it`, whose slot can be written again.
-            float *fac = reinterpret_cast<float *>(sm + kWFacOff);
+            // K block `it` is handed over once the one BUFS before it is in its accumulator: that one's MMAs
+            // waited for the promotion of the one 2 BUFS before `it`, whose slot can be written again.
+            float *fac = reinterpret_cast<float *>(sm + Cfg::OFF_FAC);
             const int rows_n = (N + 127) / 128;
-            const int total = (num_tiles - pair + npairs - 1) / npairs * num_k;
             int pt = pair, pk = 0, pslot = 0;
             const float *pa[4], *pb;
             auto aim = [&] {   // at the rows of tile pt
-                const int tm = pt / tiles_n, m0 = tm * 256 + rank * 128 + lane, nb = (pt - tm * tiles_n) * 2;
+                const int tm = pt / tiles_n, m0 = tm * 256 + rank * 128 + lane, ng = (pt - tm * tiles_n) * Cfg::GROUPS;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) pa[j] = as + (int64_t)min(m0 + 32 * j, M - 1) * num_k;
-                pb = bs + (int64_t)min(nb + (lane & 1), rows_n - 1) * num_k;
+                pb = bs + (int64_t)min((ng + (lane & 3)) / 2, rows_n - 1) * num_k;
             };
             aim();
             auto fetch = [&](int i) {
@@ -509,91 +518,84 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                     float *to = fac + pslot * kWFacPitch;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) cp_async4(to + 32 * j + lane, pa[j] + pk);
-                    if (lane < 2) cp_async4(to + 128 + lane, pb + pk);
+                    if (lane < Cfg::GROUPS) cp_async4(to + 128 + lane, pb + pk);
                     if (++pk == num_k && i + 1 < total) {
                         pk = 0;
                         pt += npairs;
                         aim();
                     }
-                    if (++pslot == kWFacSlots) pslot = 0;
+                    if (++pslot == Cfg::FAC_SLOTS) pslot = 0;
                 }
                 cp_async_commit();
             };
             for (int i = 0; i < kWFacAhead; ++i) fetch(i);
+            int b = 0;
+            uint32_t ph = 1;
             for (int it = 0; it < total; ++it) {
-                const int b = it & 1;
-                if (it >= 2 && !f8_warp_wait(&acc_full[b], (uint32_t)(((it >> 1) & 1) ^ 1), status)) break;
+                if (it >= BUFS && !f8_warp_wait(&acc_full[b], ph, status)) break;
                 fetch(it + kWFacAhead);
                 cp_async_wait<kWFacAhead>();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_full[b]);
+                if (++b == BUFS) {
+                    b = 0;
+                    ph ^= 1;
+                }
             }
             cp_async_wait<0>();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + half * 128;
+        if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        constexpr int CH = Cfg::CH, NCH = 64 / CH;
+        const int quarter = warp & 3, group = (warp - 4) >> 2;
+        const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + group * 64;
         const uint32_t leader_empty = f8_mapa(acc_empty, 0);
         const int r0 = rank * 128 + quarter * 32;
-        uint8_t *piece = sm + kWOutOff + (warp - 4) * kWPieceBytes;
-        const float *fac = reinterpret_cast<const float *>(sm + kWFacOff);
-        int fslot = 0;
-        auto factor = [&] {   // of this thread's row and half, the next K block's
-            const float f = fac[fslot * kWFacPitch + quarter * 32 + lane] * fac[fslot * kWFacPitch + 128 + half];
-            if (++fslot == kWFacSlots) fslot = 0;
-            return f;
-        };
-        int it = 0;
+        uint8_t *piece = sm + Cfg::OFF_OUT + (warp - 4) * kWPieceBytes;
+        const float *fac = reinterpret_cast<const float *>(sm + Cfg::OFF_FAC);
+        int fslot = 0, b = 0;
+        uint32_t bph = 0;
         bool ok = true;
         for (int t = pair; t < num_tiles && ok; t += npairs) {
-            float acc[4][32];
+            float acc[64];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+            for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
+            for (int k = 0; k < num_k; ++k) {
+                if (!(ok = f8_warp_wait(&acc_full[b], bph, status))) break;
+                tc_fence_after();
+                uint32_t d[2][CH];   // CH columns are loaded while the CH before are added
+                f8_tmem_ld(tm + b * BN, d[0]);
+                const float f = fac[fslot * kWFacPitch + quarter * 32 + lane] * fac[fslot * kWFacPitch + 128 + group];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) acc[c][j] = 0.0f;
-            uint32_t d[2][32];   // 32 columns are loaded while the 32 before are added, also from one K block to the next
-            ok = f8_warp_wait(&acc_full[it & 1], (uint32_t)((it >> 1) & 1), status);
-            if (!ok) break;
-            tc_fence_after();
-            tmem_ld32(tm + (it & 1) * 256, d[0]);
-            float f = factor();
-            for (int k = 0; k < num_k; ++k, ++it) {
-                const int b = it & 1;
-                const uint32_t next_ph = (uint32_t)(((it + 1) >> 1) & 1);
-                bool next = false;   // whether the next K block's accumulator is there, looked at early
-#pragma unroll
-                for (int c = 0; c < 3; ++c) {
+                for (int c = 0; c < NCH; ++c) {
                     tmem_ld_wait_for(d[c & 1]);
-                    tmem_ld32(tm + b * 256 + 32 * (c + 1), d[(c + 1) & 1]);
-                    if (c == 1) next = f8_done(&acc_full[b ^ 1], next_ph);
-                    f8_promote(acc[c], d[c & 1], f);
+                    if (c + 1 < NCH) {
+                        f8_tmem_ld(tm + b * BN + CH * (c + 1), d[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) f8_arrive_at(leader_empty + (uint32_t)(b * 8));
+                    }
+                    f8_promote(acc + CH * c, d[c & 1], f);
                 }
-                tmem_ld_wait_for(d[1]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) f8_arrive_at(leader_empty + (uint32_t)(b * 8));
-                const float f3 = f;
-                if (k + 1 < num_k) {
-                    if (!__all_sync(0xffffffffu, next) && !(ok = f8_warp_wait(&acc_full[b ^ 1], next_ph, status))) break;
-                    tc_fence_after();
-                    tmem_ld32(tm + (b ^ 1) * 256, d[0]);
-                    f = factor();
+                if (++fslot == Cfg::FAC_SLOTS) fslot = 0;
+                if (++b == BUFS) {
+                    b = 0;
+                    bph ^= 1;
                 }
-                f8_promote(acc[3], d[1], f3);
             }
             if (!ok) break;
             // a row of y lies in one thread: pieces of 32 rows x 64 bytes turn in the warp's shared memory
             // (16-byte chunk c of row r at chunk c ^ (r / 2 % 4): no bank conflicts either way) so that a store
             // covers eight runs of 64 bytes instead of 32 of 16
             constexpr int CPP = OUT_BF16 ? 32 : 16;      // columns per piece
-            const int m_base = t / tiles_n * 256 + r0, n_base = t % tiles_n * 256 + half * 128;
+            const int m_base = t / tiles_n * 256 + r0, n_base = t % tiles_n * BN + group * 64;
 #pragma unroll
-            for (int pc = 0; pc < 128 / CPP; ++pc) {
+            for (int pc = 0; pc < 64 / CPP; ++pc) {
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float *v = OUT_BF16 ? &acc[pc][8 * c] : &acc[pc / 2][16 * (pc % 2) + 4 * c];
+                    const float *v = acc + CPP * pc + CPP / 4 * c;
                     uint4 u;
                     if constexpr (OUT_BF16) {
                         uint32_t w[4];
@@ -663,28 +665,67 @@ bool f8_map(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t K, uint32_t
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MT, bool OUT_BF16>
-cudaError_t launch_narrow_t(const Fp8GemmArgs &g, cudaStream_t st) {
-    using Cfg = NarrowCfg<MT>;
-    static PerDevice<int> sm_count;   // the shared-memory attribute is set per device alongside
-    int sms = 0;
-    const cudaError_t e = sm_count.get(
-        [](int dev, int &r) {
-            cudaError_t x = cudaFuncSetAttribute(fp8_gemm_narrow_kernel<MT, OUT_BF16>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
-            if (x == cudaSuccess) x = cudaDeviceGetAttribute(&r, cudaDevAttrMultiProcessorCount, dev);
-            return x;
+// What the device runs at once: SMs, clusters of 2, 4 and 8 CTAs (a cluster lies within one GPC, so fewer than the
+// SMs allow; the query counts one CTA an SM), SM pairs of the wide kernel. Kernel attributes are set alongside.
+struct Fp8Device {
+    int sms, clusters[4], pairs;
+};
+template <typename K>
+cudaError_t f8_count_clusters(K kernel, int threads, int smem, dim3 cluster, int *count) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster.x;
+    attr.val.clusterDim.y = cluster.y;
+    attr.val.clusterDim.z = cluster.z;
+    cfg.gridDim = cluster;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(count, kernel, &cfg);
+}
+template <int MT>
+cudaError_t f8_set_narrow() {
+    const cudaError_t e = cudaFuncSetAttribute(fp8_gemm_narrow_kernel<MT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, NarrowCfg<MT>::SMEM);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(fp8_gemm_narrow_kernel<MT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, NarrowCfg<MT>::SMEM);
+}
+template <int BN>
+cudaError_t f8_set_wide() {
+    const cudaError_t e = cudaFuncSetAttribute(fp8_gemm_wide_kernel<BN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideCfg<BN>::SMEM);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(fp8_gemm_wide_kernel<BN, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideCfg<BN>::SMEM);
+}
+cudaError_t f8_device(Fp8Device *out) {
+    static PerDevice<Fp8Device> rec;
+    return rec.get(
+        [](int dev, Fp8Device &r) {
+            cudaError_t e = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev);
+            if (e == cudaSuccess) e = f8_set_narrow<16>();
+            if (e == cudaSuccess) e = f8_set_narrow<32>();
+            if (e == cudaSuccess) e = f8_set_narrow<64>();
+            if (e == cudaSuccess) e = f8_set_narrow<128>();
+            if (e == cudaSuccess) e = f8_set_wide<128>();
+            if (e == cudaSuccess) e = f8_set_wide<192>();
+            if (e == cudaSuccess) e = f8_set_wide<256>();
+            for (int i = 1; i < 4 && e == cudaSuccess; ++i)
+                e = f8_count_clusters(fp8_gemm_narrow_kernel<128, true>, NarrowCfg<128>::THREADS, NarrowCfg<128>::SMEM,
+                                      dim3(1, 1, 1u << i), &r.clusters[i]);
+            if (e == cudaSuccess)
+                e = f8_count_clusters(fp8_gemm_wide_kernel<256, true>, WideCfg<256>::THREADS, WideCfg<256>::SMEM, dim3(2), &r.pairs);
+            if (e == cudaSuccess && r.pairs < 1) e = cudaErrorInvalidConfiguration;
+            return e;
         },
-        &sms);
-    if (e != cudaSuccess) return e;
+        out);
+}
+
+template <int MT>
+cudaError_t launch_narrow(const Fp8GemmArgs &g, int split, cudaStream_t st) {
+    using Cfg = NarrowCfg<MT>;
     CUtensorMap mw, mx;
     if (!f8_map(&mw, g.bq, (uint64_t)g.N, (uint64_t)g.K, 128) || !f8_map(&mx, g.aq, (uint64_t)g.M, (uint64_t)g.K, MT))
         return cudaErrorInvalidValue;
-    const int nt = (g.N + 127) / 128, mt = (g.M + MT - 1) / MT, kb = (g.K + 127) / 128;
-    int split = 1;   // doubled while the CTAs fit at once and every range keeps two K blocks
-    while (split < 8 && (int64_t)nt * mt * split * 2 <= (int64_t)Cfg::CTAS * sms && kb >= 4 * split) split *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)nt, (unsigned)mt, (unsigned)split);
+    cfg.gridDim = dim3((unsigned)((g.N + 127) / 128), (unsigned)((g.M + MT - 1) / MT), (unsigned)split);
     cfg.blockDim = dim3(Cfg::THREADS);
     cfg.dynamicSmemBytes = Cfg::SMEM;
     cfg.stream = st;
@@ -697,61 +738,96 @@ cudaError_t launch_narrow_t(const Fp8GemmArgs &g, cudaStream_t st) {
     attrs[1].val.clusterDim.z = (unsigned)split;
     cfg.attrs = attrs;
     cfg.numAttrs = split > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_narrow_kernel<MT, OUT_BF16>, mw, mx, g.as, g.bs, g.M, g.N, kb, g.y, split,
-                              g.status);
+    const int kb = (g.K + 127) / 128;
+    if (g.out_bf16)
+        return cudaLaunchKernelEx(&cfg, fp8_gemm_narrow_kernel<MT, true>, mw, mx, g.as, g.bs, g.M, g.N, kb, g.y, split, g.status);
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_narrow_kernel<MT, false>, mw, mx, g.as, g.bs, g.M, g.N, kb, g.y, split, g.status);
 }
 
-template <int MT>
-cudaError_t launch_narrow(const Fp8GemmArgs &g, cudaStream_t st) {
-    return g.out_bf16 ? launch_narrow_t<MT, true>(g, st) : launch_narrow_t<MT, false>(g, st);
-}
-
-template <bool OUT_BF16>
-cudaError_t launch_wide(const Fp8GemmArgs &g, cudaStream_t st) {
+template <int BN>
+cudaError_t launch_wide(const Fp8GemmArgs &g, int pairs, cudaStream_t st) {
+    using Cfg = WideCfg<BN>;
+    CUtensorMap ma, mb;
+    if (!f8_map(&ma, g.aq, (uint64_t)g.M, (uint64_t)g.K, 128) || !f8_map(&mb, g.bq, (uint64_t)g.N, (uint64_t)g.K, BN / 2))
+        return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attrs[2];
-    attrs[0].id = cudaLaunchAttributeClusterDimension;
-    attrs[0].val.clusterDim.x = 2;
-    attrs[0].val.clusterDim.y = 1;
-    attrs[0].val.clusterDim.z = 1;
-    attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.blockDim = dim3(kWThreads);
-    cfg.dynamicSmemBytes = kWSmem;
+    const int64_t tiles = (int64_t)((g.N + BN - 1) / BN) * ((g.M + 255) / 256);
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.blockDim = dim3(Cfg::THREADS);
+    cfg.dynamicSmemBytes = Cfg::SMEM;
     cfg.stream = st;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = 2;
+    attrs[1].val.clusterDim.y = 1;
+    attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
     cfg.numAttrs = 2;
-    static PerDevice<int> max_pairs;   // as many pairs as run at once
-    int pairs = 0;
-    const cudaError_t e = max_pairs.get(
-        [&cfg](int, int &r) {
-            cudaError_t x = cudaFuncSetAttribute(fp8_gemm_wide_kernel<OUT_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
-            if (x != cudaSuccess) return x;
-            cudaLaunchConfig_t q = cfg;
-            q.gridDim = dim3(2);
-            int clusters = 0;
-            if ((x = cudaOccupancyMaxActiveClusters(&clusters, fp8_gemm_wide_kernel<OUT_BF16>, &q)) != cudaSuccess) return x;
-            r = clusters > 0 ? clusters : 1;
-            return cudaSuccess;
-        },
-        &pairs);
-    if (e != cudaSuccess) return e;
-    CUtensorMap ma, mb;
-    if (!f8_map(&ma, g.aq, (uint64_t)g.M, (uint64_t)g.K, 128) || !f8_map(&mb, g.bq, (uint64_t)g.N, (uint64_t)g.K, 128))
-        return cudaErrorInvalidValue;
-    const int64_t tiles = (int64_t)((g.N + 255) / 256) * ((g.M + 255) / 256);
-    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_wide_kernel<OUT_BF16>, ma, mb, g.as, g.bs, g.M, g.N, (g.K + 127) / 128, g.y, g.status);
+    const int kb = (g.K + 127) / 128;
+    if (g.out_bf16) return cudaLaunchKernelEx(&cfg, fp8_gemm_wide_kernel<BN, true>, ma, mb, g.as, g.bs, g.M, g.N, kb, g.y, g.status);
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_wide_kernel<BN, false>, ma, mb, g.as, g.bs, g.M, g.N, kb, g.y, g.status);
 }
 
 }  // namespace
 
+// The kernel and tile with the least estimated time: a start, and per wave of CTAs (or pairs) an end and a cost for
+// each K block, in us at 1965 MHz. Fitted to timings of each form at 1 to 64 K blocks (bf16 output, CUDA-graph
+// replay). Over 33 shapes of 1 to 32768 rows the pick was 1 % behind the fastest form on average, 12 % at
+// most; for example (us: narrow 64, narrow 128, wide 128, wide 192, wide 256)
+//     256 x 2048 x 4096   10.3, 12.4, 13.6, 16.0, 18.3      1024 x 2048 x 4096   25.8, 19.0, 15.1, 17.4, 19.3
+//     256 x 12352 x 2048  24.5, 21.9, 14.9, 11.6, 13.4      4096 x 1024 x 2048   30.7, 21.5, 15.4, 18.2, 13.1
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st) {
-    if (g.M > 128) return g.out_bf16 ? launch_wide<true>(g, st) : launch_wide<false>(g, st);
-    if (g.M <= 16) return launch_narrow<16>(g, st);
-    if (g.M <= 32) return launch_narrow<32>(g, st);
-    if (g.M <= 64) return launch_narrow<64>(g, st);
-    return launch_narrow<128>(g, st);
+    Fp8Device dev;
+    const cudaError_t e = f8_device(&dev);
+    if (e != cudaSuccess) return e;
+    const int kb = (g.K + 127) / 128;
+    struct Form {
+        int tile;
+        float start, end, block, push;   // push: what a split's exchange of partial sums adds
+    };
+    static const Form narrow[4] = {{16, 2.1f, 1.0f, 0.26f, 0.8f}, {32, 2.2f, 1.0f, 0.285f, 1.4f}, {64, 2.7f, 1.0f, 0.31f, 2.3f},
+                                   {128, 3.6f, 1.0f, 0.42f, 3.6f}};
+    static const Form wide[3] = {{128, 3.2f, 0.8f, 0.311f, 0.0f}, {192, 3.8f, 1.0f, 0.381f, 0.0f}, {256, 4.2f, 1.2f, 0.4275f, 0.0f}};
+    float best = 3.0e38f;
+    int form = 0, split = 1;
+    const int64_t nt = (g.N + 127) / 128;
+    for (int i = 0; i < 4; ++i) {
+        const int64_t ctas = nt * ((g.M + narrow[i].tile - 1) / narrow[i].tile);
+        // K split as far as there is an SM for every CTA, all clusters run at once and every CTA keeps two K blocks
+        int lg = 0;
+        while (lg < 3 && ctas * (2 << lg) <= dev.sms && ctas <= (int64_t)(narrow[i].tile <= 32 ? 2 : 1) * dev.clusters[lg + 1] &&
+               kb >= 4 << lg)
+            ++lg;
+        const int64_t waves = ((ctas << lg) + dev.sms - 1) / dev.sms;
+        const float t = narrow[i].start + (float)waves * (narrow[i].end + (float)((kb + (1 << lg) - 1) >> lg) * narrow[i].block) +
+                        (lg ? narrow[i].push : 0.0f);
+        if (t < best) {
+            best = t;
+            form = i;
+            split = 1 << lg;
+        }
+        if (narrow[i].tile >= g.M) break;   // wider tiles hold nothing more
+    }
+    for (int i = 0; i < 3 && g.M > 64; ++i) {
+        const int64_t tiles = (int64_t)((g.N + wide[i].tile - 1) / wide[i].tile) * ((g.M + 255) / 256);
+        const int64_t waves = (tiles + dev.pairs - 1) / dev.pairs;
+        const float t = wide[i].start + (float)waves * (wide[i].end + (float)kb * wide[i].block);
+        if (t < best) {
+            best = t;
+            form = 4 + i;
+        }
+    }
+    switch (form) {
+        case 0: return launch_narrow<16>(g, split, st);
+        case 1: return launch_narrow<32>(g, split, st);
+        case 2: return launch_narrow<64>(g, split, st);
+        case 3: return launch_narrow<128>(g, split, st);
+        case 4: return launch_wide<128>(g, dev.pairs, st);
+        case 5: return launch_wide<192>(g, dev.pairs, st);
+        default: return launch_wide<256>(g, dev.pairs, st);
+    }
 }
 
 }  // namespace gdn
