@@ -323,7 +323,7 @@ gdn_status q4k_gemm(const void *a, const uint8_t *w, int32_t M, int32_t N, int32
 static gdn_status fp8_quantize(const void *x, int64_t ldx, gdn_dtype in_dtype, bool weight, int32_t rows, int32_t K,
                                uint8_t *xq, float *xs, gdn_stream_t stream) {
     if (rows < 0 || K < 0 || ldx < K || !dtype_ok(in_dtype)) return GDN_ERR_INVALID_ARG;
-    if (K % 16 != 0) return GDN_ERR_UNSUPPORTED;
+    if (K % 16 != 0 || K > INT32_MAX - 255 || rows > INT32_MAX - 255) return GDN_ERR_UNSUPPORTED;
     if (rows == 0 || K == 0) return GDN_OK;
     if ((int64_t)rows * ((K + 127) / 128) > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     if (!x || !xq || !xs || !aligned16(x) || !aligned16(xq) || ldx % (in_dtype == GDN_BF16 ? 8 : 4) != 0)
@@ -358,7 +358,8 @@ gdn_status gdn_gated_rmsnorm_silu_fp8(const void *o, const void *z, const float 
 gdn_status fp8_gemm(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs, int32_t M, int32_t N,
                     int32_t K, gdn_dtype out_dtype, void *y, gdn_stream_t stream) {
     if (M < 0 || N < 0 || K < 0 || !dtype_ok(out_dtype)) return GDN_ERR_INVALID_ARG;
-    if (K % 16 != 0 || N % 16 != 0 || M > 128 * 65535) return GDN_ERR_UNSUPPORTED;
+    if (K % 16 != 0 || N % 16 != 0 || M > 128 * 65535 || K > INT32_MAX - 255 || N > INT32_MAX - 255)
+        return GDN_ERR_UNSUPPORTED;
     if (M == 0 || N == 0) return GDN_OK;
     if (K == 0) return GDN_ERR_UNSUPPORTED;
     if (!aq || !as || !bq || !bs || !y) return GDN_ERR_INVALID_ARG;

@@ -221,6 +221,7 @@ struct PooledDecodeArgs {
     uint8_t *xq;                 // [B, Hv * 128] E4M3 or null (no tail)
     float *xs;                   // [B, Hv]
     int *status;
+    int32_t unit_heads;          // set by the launcher
 };
 cudaError_t launch_decode_pooled(const PooledDecodeArgs &d, cudaStream_t st);
 

@@ -4,10 +4,12 @@
 // "Why Gated DeltaNet Survives 4-Bit Quantization" (abstract, mechanisms ii-iii); tail: "Red Lite dev15d -
 // DeltaNet gated tail", Pinned graph semantics, steps 1-5.
 //
-// HBM-bound: 128 KB of state traffic and about 8 operations a state value per (row, head). Persistent, one CTA
-// per SM over an equal share of the (row, head) items; a producer warp brings each item's 64 KB state and its
-// q, k, v, z rows into a three-stage ring by bulk copies, so loads stay in flight while items are
-// computed, written back and encoded:
+// HBM-bound: 128 KB of state traffic and about 8 operations a state value per (row, head) item. The grid has one
+// CTA per unit of one or more heads of a row; those that run take over the units of CTAs that have not been
+// launched yet (cluster launch control), so each SM does as many as its share of the memory rate allows (equal
+// shares left the fastest SMs idle for a fifth of the time: 188 us against KKK for 256 rows x 32 heads). A
+// producer warp brings each item's 64 KB state and its q, k, v, z rows into a ring by bulk copies, so loads
+// stay in flight while items are computed, written back and encoded:
 //   warps 0-7   the state from the stage into registers (8 lanes a row, 4 rows a thread, the layout and
 //               arithmetic of gdn_recurrent128_kernel, so o and S equal gdn_decode_step's bit for bit), the
 //               stage released at once, the update, S stored straight to the pool, o to shared memory;
@@ -43,7 +45,8 @@ struct PoolSmem {
     __nv_bfloat16 q[kPoolStages][kD], k[kPoolStages][kD], v[kPoolStages][kD], z[kPoolStages][kD];
     float o[kPoolRows][kD];
     PoolMeta meta[kPoolStages];
-    uint64_t full[kPoolStages], empty[kPoolStages], o_full[kPoolRows], o_empty[kPoolRows];
+    uint4 claim;               // answer of the launch control
+    uint64_t full[kPoolStages], empty[kPoolStages], o_full[kPoolRows], o_empty[kPoolRows], claimed;
 };
 constexpr int kPoolSmem = (int)sizeof(PoolSmem) + 128;
 
@@ -52,6 +55,31 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                      smem_u32(dst)),
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
+}
+
+// Asks for the unit of a CTA that has not been launched: the answer (16 bytes) completes on `bar`.
+__device__ __forceinline__ void claim_unit(uint4 *answer, uint64_t *bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The claimed unit (that CTA's index), or -1 if none was left.
+__device__ __forceinline__ int claimed_unit(const uint4 *answer) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    fence_proxy_async_smem();   // read before the next answer is written
+    return ok ? (int)x : -1;
 }
 
 __device__ __forceinline__ float pool_dot16(const f2_t (&a)[8], const f2_t (&b)[8]) {
@@ -100,13 +128,14 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
         for (int s = 0; s < kPoolStages; ++s) {
-            mbar_init(&sm.full[s], 1);
+            mbar_init(&sm.full[s], 2);   // the copies, and the item's meta data
             mbar_init(&sm.empty[s], kPoolWarps + 1);
         }
         for (int b = 0; b < kPoolRows; ++b) {
             mbar_init(&sm.o_full[b], kPoolWarps);
             mbar_init(&sm.o_empty[b], 1);
         }
+        mbar_init(&sm.claimed, 1);
         fence_barrier_init();
     }
     __syncthreads();
@@ -114,47 +143,43 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
     const int Hv = d.Hv;
 
     if (warp == kPoolWarps) {
-        const int64_t items = (int64_t)d.B * Hv;
-        const int first = (int)(items * blockIdx.x / gridDim.x), last = (int)(items * (blockIdx.x + 1) / gridDim.x);
-        const int group = Hv / d.Hk;
-        int it = 0, row = -1, slot = -1;
+        const int group = Hv / d.Hk, units_row = (Hv + d.unit_heads - 1) / d.unit_heads;
+        int it = 0, claims = 0;
         bool ok = true;
-        for (int item = first; item < last && ok; ++item) {
-            if (item / Hv != row) {
-                row = item / Hv;
-                slot = d.slots[row];
-                bool seen = false;
-                for (int i = lane; i < row; i += 32) seen |= d.slots[i] == slot;
-                seen = __any_sync(kAll, seen);
-                if (slot >= 0 && (slot >= d.num_slots || seen)) {
-                    if (lane == 0) report_status(d.status, GDN_ERR_INVALID_ARG);
-                    slot = -1;
+        for (int unit = blockIdx.x; unit >= 0 && ok;) {
+            if (lane == 0) claim_unit(&sm.claim, &sm.claimed);   // the next one
+            ++claims;
+            const int row = unit / units_row, h0 = (unit - row * units_row) * d.unit_heads;
+            const int slot = d.slots[row];
+            bool again = false;
+            for (int i = lane; i < row; i += 32) again |= d.slots[i] == slot;   // an earlier row's slot
+            again = __any_sync(kAll, again);
+            const bool live = slot >= 0 && slot < d.num_slots && !again;
+            if (slot >= 0 && !live && lane == 0) report_status(d.status, GDN_ERR_INVALID_ARG);
+            for (int h = h0; live && h < min(h0 + d.unit_heads, Hv); ++h, ++it) {
+                const int s = it % kPoolStages;
+                ok = warp_wait(&sm.empty[s], (uint32_t)(((it / kPoolStages) & 1) ^ 1), lane, d.status);
+                if (!ok) break;
+                if (lane == 0) {
+                    const int64_t vrow = ((int64_t)row * Hv + h) * kD, krow = ((int64_t)row * d.Hk + h / group) * kD;
+                    mbar_arrive_expect_tx(&sm.full[s], kStateBytes + (TAIL ? 4 : 3) * kRowBytes);
+                    bulk_load(sm.state[s], d.pool + ((int64_t)slot * Hv + h) * kD * kD, kStateBytes, &sm.full[s]);
+                    bulk_load(sm.k[s], reinterpret_cast<const __nv_bfloat16 *>(d.k) + krow, kRowBytes, &sm.full[s]);
+                    bulk_load(sm.q[s], reinterpret_cast<const __nv_bfloat16 *>(d.q) + krow, kRowBytes, &sm.full[s]);
+                    bulk_load(sm.v[s], reinterpret_cast<const __nv_bfloat16 *>(d.v) + vrow, kRowBytes, &sm.full[s]);
+                    if constexpr (TAIL)
+                        bulk_load(sm.z[s], reinterpret_cast<const __nv_bfloat16 *>(d.z) + row * d.ldz + h * kD, kRowBytes, &sm.full[s]);
+                    float g, beta;   // while the state is on its way
+                    gdn_gates(gate_at(d.a, d.gate_bf16, row * d.ldg + h), gate_at(d.b, d.gate_bf16, row * d.ldg + h), d.A_log[h],
+                              d.dt_bias[h], g, beta);
+                    sm.meta[s] = {row, h, slot, expf(g), beta};
+                    mbar_arrive(&sm.full[s]);
                 }
+                __syncwarp();
             }
-            if (slot < 0) {
-                item = (row + 1) * Hv - 1;   // the next row
-                continue;
-            }
-            const int h = item - row * Hv, s = it % kPoolStages;
-            ok = warp_wait(&sm.empty[s], (uint32_t)(((it / kPoolStages) & 1) ^ 1), lane, d.status);
-            if (!ok) break;
-            if (lane == 0) {
-                const int64_t vrow = ((int64_t)row * Hv + h) * kD, krow = ((int64_t)row * d.Hk + h / group) * kD;
-                float g, beta;
-                gdn_gates(gate_at(d.a, d.gate_bf16, row * d.ldg + h), gate_at(d.b, d.gate_bf16, row * d.ldg + h), d.A_log[h],
-                          d.dt_bias[h], g, beta);
-                sm.meta[s] = {row, h, slot, expf(g), beta};
-                mbar_arrive_expect_tx(&sm.full[s], kStateBytes + (TAIL ? 4 : 3) * kRowBytes);
-                bulk_load(sm.state[s], d.pool + ((int64_t)slot * Hv + h) * kD * kD, kStateBytes, &sm.full[s]);
-                bulk_load(sm.k[s], reinterpret_cast<const __nv_bfloat16 *>(d.k) + krow, kRowBytes, &sm.full[s]);
-                bulk_load(sm.q[s], reinterpret_cast<const __nv_bfloat16 *>(d.q) + krow, kRowBytes, &sm.full[s]);
-                bulk_load(sm.v[s], reinterpret_cast<const __nv_bfloat16 *>(d.v) + vrow, kRowBytes, &sm.full[s]);
-                if constexpr (TAIL)
-                    bulk_load(sm.z[s], reinterpret_cast<const __nv_bfloat16 *>(d.z) + row * d.ldz + h * kD, kRowBytes,
-                              &sm.full[s]);
-            }
+            if (!warp_wait(&sm.claimed, (uint32_t)((claims - 1) & 1), lane, d.status)) break;
+            unit = claimed_unit(&sm.claim);
             __syncwarp();
-            ++it;
         }
         // before the warp ends every copy it armed has landed; then one end mark for each finisher
         if (lane == 0) {
@@ -167,6 +192,7 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
                 ok = mbar_wait(&sm.empty[s], (uint32_t)(((e / kPoolStages) & 1) ^ 1), d.status);
                 if (!ok) break;
                 sm.meta[s].row = -1;
+                mbar_arrive(&sm.full[s]);
                 mbar_arrive(&sm.full[s]);
             }
         }
@@ -284,7 +310,7 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
 }
 
 template <bool TAIL>
-cudaError_t launch_pooled_t(const PooledDecodeArgs &d, cudaStream_t st) {
+cudaError_t launch_pooled_t(PooledDecodeArgs d, cudaStream_t st) {
     static PerDevice<int> sm_count;   // the shared-memory attribute is set per device alongside
     int sms = 0;
     const cudaError_t e = sm_count.get(
@@ -296,9 +322,12 @@ cudaError_t launch_pooled_t(const PooledDecodeArgs &d, cudaStream_t st) {
         },
         &sms);
     if (e != cudaSuccess) return e;
-    const int64_t items = (int64_t)d.B * d.Hv;
-    return launch_pdl(gdn_decode128_pooled_kernel<TAIL>, dim3((unsigned)(items < sms ? items : sms)), dim3(kPoolThreads),
-                      kPoolSmem, st, d);
+    // heads per unit: doubled while every SM keeps sixteen units or more (each looks through the batch's slots once)
+    d.unit_heads = 1;
+    while (d.unit_heads < d.Hv && (int64_t)d.B * ((d.Hv + 2 * d.unit_heads - 1) / (2 * d.unit_heads)) >= 16 * (int64_t)sms)
+        d.unit_heads *= 2;
+    const int64_t units = (int64_t)d.B * ((d.Hv + d.unit_heads - 1) / d.unit_heads);
+    return launch_pdl(gdn_decode128_pooled_kernel<TAIL>, dim3((unsigned)units), dim3(kPoolThreads), kPoolSmem, st, d);
 }
 
 }  // namespace
