@@ -10,13 +10,17 @@
 // shares left the fastest SMs idle for a fifth of the time: 188 us against KKK for 256 rows x 32 heads). A
 // producer warp brings each item's 64 KB state and its q, k, v, z rows into a ring by bulk copies, so loads
 // stay in flight while items are computed, written back and encoded:
-//   warps 0-7   the state from the stage into registers (8 lanes a row, 4 rows a thread, the layout and
-//               arithmetic of gdn_recurrent128_kernel, so o and S equal gdn_decode_step's bit for bit), the
-//               stage released at once, the update, S stored straight to the pool, o to shared memory;
-//   warp 8      slots, bulk copies, gates;
-//   warps 9-10  item i's o row on warp 9 + i % 2 (tail and encode, or the plain store). Its chain of
-//               reductions and divisions takes longer than the update; done in turn by the update's own warps
-//               it held up every item's last row (6.5 us an item against 3 us of HBM time).
+//   warps 0-15   the state from the stage into registers (8 lanes a row, 2 rows a thread, in the arithmetic of
+//                gdn_recurrent128_kernel, so o and S equal gdn_decode_step's bit for bit), the stage released
+//                at once, the update, S stored straight to the pool, o to shared memory;
+//   warp 16      slots, bulk copies, gates;
+//   warps 17-18  item i's o row on warp 17 + i % 2 (tail and encode, or the plain store). Its chain of
+//                reductions and divisions takes longer than the update; done in turn by the update's own warps
+//                it held up every item's last row (6.5 us an item against 3 us of HBM time).
+// Both kinds of item warps go through their loop once before their first item, on whatever shared memory holds and
+// without a wait or a store: it brings the loop's code into the SM's instruction cache while the first state is on
+// its way. Without it a CTA's first item took 12,700 cycles from its state's arrival to its codes, later ones a
+// third of that, which is most of a small batch's time.
 // A row with a negative slot is passed over (its outputs stay as they are); so is a row whose slot is not
 // below num_slots or is named by an earlier row, and the status word then reads GDN_ERR_INVALID_ARG.
 // Every wait is bounded; an expired one records GDN_ERR_TIMEOUT and the warp ends.
@@ -28,7 +32,7 @@ namespace {
 
 constexpr int kD = 128;
 constexpr int kPoolStages = 3;
-constexpr int kPoolWarps = 8;
+constexpr int kPoolWarps = 16;
 constexpr int kPoolFinishers = 2;
 constexpr int kPoolRows = 4;               // o rows between the update and the finishers
 constexpr int kPoolThreads = 32 * (kPoolWarps + 1 + kPoolFinishers);
@@ -88,13 +92,12 @@ __device__ __forceinline__ float pool_dot16(const f2_t (&a)[8], const f2_t (&b)[
     for (int c = 1; c < 8; ++c) acc = fma2(a[c], b[c], acc);
     return f2lo(acc) + f2hi(acc);
 }
-// The sum over a row group of 8 lanes of four values: lanes whose bits 2 and 1 are (p >> 1, p & 1) get value p.
-__device__ __forceinline__ float pool_sum4(const float (&x)[4], int l8) {
-    const bool b2 = (l8 & 4) != 0, b1 = (l8 & 2) != 0;
-    const float r0 = __shfl_xor_sync(kAll, b2 ? x[0] : x[2], 4);
-    const float r1 = __shfl_xor_sync(kAll, b2 ? x[1] : x[3], 4);
-    const float k0 = (b2 ? x[2] : x[0]) + r0, k1 = (b2 ? x[3] : x[1]) + r1;
-    float v = (b1 ? k1 : k0) + __shfl_xor_sync(kAll, b1 ? k0 : k1, 2);
+// The sums over a row group of 8 lanes of two values: lanes whose bit 2 is p get value p. (In the order of additions of
+// the four-row form of gdn_recurrent128_kernel.)
+__device__ __forceinline__ float pool_sum2(const float (&x)[2], int l8) {
+    const bool b2 = (l8 & 4) != 0;
+    float v = (b2 ? x[1] : x[0]) + __shfl_xor_sync(kAll, b2 ? x[0] : x[1], 4);
+    v += __shfl_xor_sync(kAll, v, 2);
     v += __shfl_xor_sync(kAll, v, 1);
     return v;
 }
@@ -139,10 +142,12 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
         fence_barrier_init();
     }
     __syncthreads();
-    pdl_wait();
     const int Hv = d.Hv;
+    int first = -1;                    // the pass before the first item
+    asm volatile("" : "+r"(first));    // (not known to the compiler, which would give that pass code of its own)
 
     if (warp == kPoolWarps) {
+        pdl_wait();
         const int group = Hv / d.Hk, units_row = (Hv + d.unit_heads - 1) / d.unit_heads;
         int it = 0, claims = 0;
         bool ok = true;
@@ -201,27 +206,25 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
 
     if (warp > kPoolWarps) {
         const int col = (lane & 15) * 8;   // lanes 16-31 repeat the row, their results unused
-        f2_t w2[4];
-        if constexpr (TAIL) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w2[j] = f2(d.norm_w[col + 2 * j], d.norm_w[col + 2 * j + 1]);
-        }
-        for (int it = warp - kPoolWarps - 1;; it += kPoolFinishers) {
-            const int s = it % kPoolStages, ob = it % kPoolRows;
-            if (!warp_wait(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), lane, d.status)) break;
+        f2_t w2[4] = {0ull, 0ull, 0ull, 0ull};
+        for (int it = first, step = warp - kPoolWarps;; it += step, step = kPoolFinishers) {
+            const bool run = it >= 0;
+            const int s = run ? it % kPoolStages : 0, ob = run ? it % kPoolRows : 0;
+            if (run && !warp_wait(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), lane, d.status)) break;
             const int row = sm.meta[s].row, head = sm.meta[s].head;
-            if (row < 0) break;
+            if (run && row < 0) break;
             uint4 zu = make_uint4(0u, 0u, 0u, 0u);
             if constexpr (TAIL) zu = *reinterpret_cast<const uint4 *>(&sm.z[s][col]);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.empty[s]);
-            if (!warp_wait(&sm.o_full[ob], (uint32_t)((it / kPoolRows) & 1), lane, d.status)) break;
+            if (run && lane == 0) mbar_arrive(&sm.empty[s]);
+            if (run && !warp_wait(&sm.o_full[ob], (uint32_t)((it / kPoolRows) & 1), lane, d.status)) break;
             const float4 oa = *reinterpret_cast<const float4 *>(&sm.o[ob][col]);
             const float4 oc = *reinterpret_cast<const float4 *>(&sm.o[ob][col + 4]);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.o_empty[ob]);
+            if (run && lane == 0) mbar_arrive(&sm.o_empty[ob]);
             const int64_t at = ((int64_t)row * Hv + head) * kD;
-            if (d.o && lane < 16) {
+            const bool store = run && lane < 16;
+            if (d.o && store) {
                 const float x[8] = {oa.x, oa.y, oa.z, oa.w, oc.x, oc.y, oc.z, oc.w};
                 if (d.out_bf16) store8<true>(d.o, at + col, x);
                 else store8<false>(d.o, at + col, x);
@@ -237,39 +240,46 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
 #pragma unroll
                 for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
                 const float sc = fp8_block_scale(amax, r);
-                if (lane < 16)
-                    *reinterpret_cast<uint2 *>(d.xq + at + col) =
-                        make_uint2(fp8_pack4(f2lo(y2[0]), f2hi(y2[0]), f2lo(y2[1]), f2hi(y2[1]), r),
-                                   fp8_pack4(f2lo(y2[2]), f2hi(y2[2]), f2lo(y2[3]), f2hi(y2[3]), r));
-                if (lane == 0) d.xs[at / kD] = sc;
+                const uint2 codes = make_uint2(fp8_pack4(f2lo(y2[0]), f2hi(y2[0]), f2lo(y2[1]), f2hi(y2[1]), r),
+                                               fp8_pack4(f2lo(y2[2]), f2hi(y2[2]), f2lo(y2[3]), f2hi(y2[3]), r));
+                if (store) *reinterpret_cast<uint2 *>(d.xq + at + col) = codes;
+                if (run && lane == 0) d.xs[at / kD] = sc;
+                if (!run) {
+                    pdl_wait();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w2[j] = f2(d.norm_w[col + 2 * j], d.norm_w[col + 2 * j + 1]);
+                }
+            } else if (!run) {
+                pdl_wait();
             }
         }
         return;
     }
 
-    const int l8 = tid & 7, rbase = (tid >> 7) * 64 + ((tid & 127) >> 3), gbase = lane & ~7;
-    for (int it = 0;; ++it) {
-        const int s = it % kPoolStages, ob = it % kPoolRows;
-        if (!warp_wait(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), lane, d.status)) break;
+    const int l8 = tid & 7, rbase = tid >> 3, gbase = lane & ~7;   // rows rbase and rbase + 64
+    for (int it = first;; ++it) {
+        const bool run = it >= 0;
+        const int s = run ? it % kPoolStages : 0, ob = run ? it % kPoolRows : 0;
+        if (run && !warp_wait(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), lane, d.status)) break;
         const PoolMeta m = sm.meta[s];
-        if (m.row < 0) break;
+        if (run && m.row < 0) break;
 
-        f2_t st[4][8], k2[8], q2[8];
+        f2_t st[2][8], k2[8], q2[8];
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float4 x = *reinterpret_cast<const float4 *>(&sm.state[s][(rbase + 16 * p) * kD + 32 * j + 4 * l8]);
+                const float4 x = *reinterpret_cast<const float4 *>(&sm.state[s][(rbase + 64 * p) * kD + 32 * j + 4 * l8]);
                 st[p][2 * j] = f2(x.x, x.y);
                 st[p][2 * j + 1] = f2(x.z, x.w);
             }
         pool_cols16(sm.k[s], l8, k2);
         pool_cols16(sm.q[s], l8, q2);
-        float vv[4];
+        float vv[2];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) vv[p] = __bfloat162float(sm.v[s][rbase + 16 * p]);
+        for (int p = 0; p < 2; ++p) vv[p] = __bfloat162float(sm.v[s][rbase + 64 * p]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.empty[s]);
+        if (run && lane == 0) mbar_arrive(&sm.empty[s]);
 
         float kn = 1.0f, qn = d.scale;
         if (d.l2norm) {
@@ -277,35 +287,38 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
             kn = rsqrtf(ks + 1e-6f);
             qn = rsqrtf(qs + 1e-6f) * d.scale;
         }
-        float part[4], sk[4];
+        float part[2], sk[2];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) part[p] = pool_dot16(st[p], k2);
-        const float skt = pool_sum4(part, l8);
+        for (int p = 0; p < 2; ++p) part[p] = pool_dot16(st[p], k2);
+        const float skt = pool_sum2(part, l8);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) sk[p] = __shfl_sync(kAll, skt, gbase + 4 * (p >> 1) + 2 * (p & 1));
+        for (int p = 0; p < 2; ++p) sk[p] = __shfl_sync(kAll, skt, gbase + 4 * p);
         const f2_t a2 = f2(m.alpha, m.alpha);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
+        for (int p = 0; p < 2; ++p) {
             const float u = m.beta * (vv[p] - m.alpha * kn * sk[p]) * kn;
             const f2_t u2 = f2(u, u);
 #pragma unroll
             for (int c = 0; c < 8; ++c) st[p][c] = fma2(a2, st[p][c], mul2(u2, k2[c]));
         }
-        float *out = d.pool + ((int64_t)m.slot * Hv + m.head) * kD * kD + rbase * kD + 4 * l8;
+        if (run) {
+            float *out = d.pool + ((int64_t)m.slot * Hv + m.head) * kD * kD + rbase * kD + 4 * l8;
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                __stcs(reinterpret_cast<float4 *>(out + 16 * p * kD + 32 * j),
-                       make_float4(f2lo(st[p][2 * j]), f2hi(st[p][2 * j]), f2lo(st[p][2 * j + 1]), f2hi(st[p][2 * j + 1])));
+                for (int j = 0; j < 4; ++j)
+                    __stcs(reinterpret_cast<float4 *>(out + 64 * p * kD + 32 * j),
+                           make_float4(f2lo(st[p][2 * j]), f2hi(st[p][2 * j]), f2lo(st[p][2 * j + 1]), f2hi(st[p][2 * j + 1])));
+        }
 #pragma unroll
-        for (int p = 0; p < 4; ++p) part[p] = pool_dot16(st[p], q2);
-        const float ot = pool_sum4(part, l8) * qn;
+        for (int p = 0; p < 2; ++p) part[p] = pool_dot16(st[p], q2);
+        const float ot = pool_sum2(part, l8) * qn;
         // the row that this buffer held has been finished
-        if (!warp_wait(&sm.o_empty[ob], (uint32_t)(((it / kPoolRows) & 1) ^ 1), lane, d.status)) break;
-        if ((l8 & 1) == 0) sm.o[ob][rbase + 16 * (2 * ((l8 >> 2) & 1) + ((l8 >> 1) & 1))] = ot;
+        if (run && !warp_wait(&sm.o_empty[ob], (uint32_t)(((it / kPoolRows) & 1) ^ 1), lane, d.status)) break;
+        if (run && (l8 & 3) == 0) sm.o[ob][rbase + 64 * (l8 >> 2)] = ot;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.o_full[ob]);
+        if (run && lane == 0) mbar_arrive(&sm.o_full[ob]);
+        if (!run) pdl_wait();
     }
 }
 
