@@ -4,9 +4,11 @@
 //     s = max(amax / 448, 2^-126),   code_j = E4M3(x_j / s)   (as x_j * (1 / s), saturating),
 // so E4M3(code_j) * s stands for x_j. All of it in fp32.
 //
-// All three are HBM-bound streams (about 3 to 12 operations a value): a block of 128 values of a row is
-// 16 lanes of 8 values, so its maximum is four shuffles, a warp's loads are 512 or 1024 consecutive
-// bytes, and every thread issues the loads of several blocks before it uses any.
+// All three are HBM-bound streams, with arithmetic close behind: with 8 bf16 values a thread the scale, the index and
+// the reductions were most of 11 instructions a value (tail of 32768 x 32 heads 131 us). So a lane takes 32 bytes of a
+// block, one wide load: 16 bf16 values (8 lanes a block: 116 us, 89 % of the measured copy rate; encoder 96 %) or 8
+// fp32 ones (16 lanes; 16 values a lane there took 124 us against 96 at 16384 rows). Long inputs go four blocks a
+// thread, all loads before any use; short ones one block a thread (256 x 2048: 1.7 us against 2.8).
 #include "common.cuh"
 #include "kernels.h"
 
@@ -14,31 +16,46 @@ namespace gdn {
 namespace {
 
 constexpr int kFp8Threads = 256;
-constexpr int kFp8Lanes = 16;                            // lanes per block of 128 values
-constexpr int kFp8Blocks = kFp8Threads / kFp8Lanes;      // blocks per CTA pass
-constexpr int kFp8Unroll = 4;
+constexpr int kFp8Long = 4;                              // blocks per thread and turn for long inputs
 
-// Eight consecutive values as loaded, or zeros.
+// Layout of a block of 128 values by input type: NC chunks of 8 values (32 bytes) a lane.
+template <bool BF16>
+struct Fp8Lay {
+    static constexpr int NC = BF16 ? 2 : 1;
+    static constexpr int LANES = 16 / NC;
+    static constexpr int BLOCKS = kFp8Threads / LANES;   // blocks per CTA pass
+};
+
+__device__ __forceinline__ void ld_global_32b(const void *p, uint32_t (&r)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+}
+
+// A lane's 32 bytes as loaded (WIDE: they are 32-byte aligned), or zeros.
 template <bool BF16>
 struct Fp8In {
-    uint4 a, b;
+    uint32_t w[8];
+    template <bool WIDE>
     __device__ __forceinline__ void load(const void *base, int64_t idx, bool live) {
-        a = b = make_uint4(0u, 0u, 0u, 0u);
-        if (!live) return;
-        if constexpr (BF16) {
-            a = *reinterpret_cast<const uint4 *>(reinterpret_cast<const __nv_bfloat16 *>(base) + idx);
+        const uint8_t *p = reinterpret_cast<const uint8_t *>(base) + idx * (BF16 ? 2 : 4);
+        if (!live) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 0u;
+        } else if constexpr (WIDE) {
+            ld_global_32b(p, w);
         } else {
-            const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const float *>(base) + idx);
-            a = p[0];
-            b = p[1];
+            const uint4 a = reinterpret_cast<const uint4 *>(p)[0], b = reinterpret_cast<const uint4 *>(p)[1];
+            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+            w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
         }
     }
-    __device__ __forceinline__ void get(f2_t (&v)[4]) const {
-        if constexpr (BF16) {
-            v[0] = bf16x2_to_f2(a.x); v[1] = bf16x2_to_f2(a.y); v[2] = bf16x2_to_f2(a.z); v[3] = bf16x2_to_f2(a.w);
-        } else {
-            v[0] = f2(__uint_as_float(a.x), __uint_as_float(a.y)); v[1] = f2(__uint_as_float(a.z), __uint_as_float(a.w));
-            v[2] = f2(__uint_as_float(b.x), __uint_as_float(b.y)); v[3] = f2(__uint_as_float(b.z), __uint_as_float(b.w));
+    // chunk c: eight values
+    __device__ __forceinline__ void get(int c, f2_t (&v)[4]) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (BF16) v[k] = bf16x2_to_f2(w[4 * c + k]);
+            else v[k] = f2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
         }
     }
 };
@@ -53,26 +70,37 @@ __device__ __forceinline__ uint2 pack8_f2(const f2_t (&v)[4], float r) {
     return make_uint2(fp8_pack4(f2lo(v[0]), f2hi(v[0]), f2lo(v[1]), f2hi(v[1]), r),
                       fp8_pack4(f2lo(v[2]), f2hi(v[2]), f2lo(v[3]), f2hi(v[3]), r));
 }
+template <int NC>
+__device__ __forceinline__ void store_codes(uint8_t *p, const f2_t (&v)[NC][4], float r) {
+    const uint2 x = pack8_f2(v[0], r);
+    if constexpr (NC == 2) {
+        const uint2 y = pack8_f2(v[1], r);
+        *reinterpret_cast<uint4 *>(p) = make_uint4(x.x, x.y, y.x, y.y);
+    } else {
+        *reinterpret_cast<uint2 *>(p) = x;
+    }
+}
 
-// Maximum over the 16 lanes of a block (all lanes of the warp take part).
-__device__ __forceinline__ float group16_max(float m) {
+// Maximum over the lanes of a block (all lanes of the warp take part).
+template <int LANES>
+__device__ __forceinline__ float block_max(float m) {
 #pragma unroll
-    for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    for (int off = LANES / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     return m;
 }
 
 // Block i of x is row i / kb, values 128 (i % kb) ..; the last block of a row may be short (K % 16 == 0,
-// so a lane's eight values are all inside or all outside).
-template <bool BF16>
-__global__ void __launch_bounds__(kFp8Threads)
+// so a lane's values are all inside or all outside).
+template <bool BF16, bool WIDE, int U>
+__global__ void __launch_bounds__(kFp8Threads, BF16 ? 3 : 4)
 fp8_quantize_act_kernel(const void *__restrict__ x, int64_t ldx, int32_t nblocks, int32_t kb, int32_t K,
                         uint8_t *__restrict__ xq, float *__restrict__ xs) {
+    using L = Fp8Lay<BF16>;
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int U = kFp8Unroll;
-    const int l = threadIdx.x % kFp8Lanes;
-    const int64_t stride = (int64_t)gridDim.x * kFp8Blocks;
-    const int64_t first = (int64_t)blockIdx.x * kFp8Blocks;
+    const int l = threadIdx.x % L::LANES;
+    const int64_t stride = (int64_t)gridDim.x * L::BLOCKS;
+    const int64_t first = (int64_t)blockIdx.x * L::BLOCKS;
     // the loop condition is uniform over the CTA (the shuffles need whole warps)
     for (int64_t i0 = first; i0 < nblocks; i0 += U * stride) {
         Fp8In<BF16> in[U];
@@ -80,49 +108,58 @@ fp8_quantize_act_kernel(const void *__restrict__ x, int64_t ldx, int32_t nblocks
         bool live[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + u * stride + threadIdx.x / kFp8Lanes;
+            const int64_t i = i0 + u * stride + threadIdx.x / L::LANES;
             row[u] = (int32_t)min(i, (int64_t)nblocks - 1) / kb;
-            col[u] = ((int32_t)min(i, (int64_t)nblocks - 1) - row[u] * kb) * 128 + 8 * l;
+            col[u] = ((int32_t)min(i, (int64_t)nblocks - 1) - row[u] * kb) * 128 + 8 * L::NC * l;
             live[u] = i < nblocks && col[u] < K;
-            in[u].load(x, row[u] * ldx + col[u], live[u]);
+            in[u].template load<WIDE>(x, row[u] * ldx + col[u], live[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            f2_t v[4];
-            in[u].get(v);
-            float r;
-            const float s = fp8_block_scale(group16_max(amax_f2(v)), r);
+            f2_t v[L::NC][4];
+            float m = 0.0f, r;
+#pragma unroll
+            for (int c = 0; c < L::NC; ++c) {
+                in[u].get(c, v[c]);
+                m = fmaxf(m, amax_f2(v[c]));
+            }
+            const float s = fp8_block_scale(block_max<L::LANES>(m), r);
             if (!live[u]) continue;
-            *reinterpret_cast<uint2 *>(xq + (int64_t)row[u] * K + col[u]) = pack8_f2(v, r);
+            store_codes<L::NC>(xq + (int64_t)row[u] * K + col[u], v, r);
             if (l == 0) xs[(int64_t)row[u] * kb + col[u] / 128] = s;
         }
     }
 }
 
-// One CTA per 128 x 128 block of w [N, K]: 16 lanes a row, 16 rows a pass, eight passes held in
-// registers between the maximum and the encoding, so w is read once.
-template <bool BF16>
-__global__ void __launch_bounds__(kFp8Threads)
+// One CTA per 128 x 128 block of w [N, K], held in registers between the maximum and the encoding, so w is
+// read once.
+template <bool BF16, bool WIDE>
+__global__ void __launch_bounds__(kFp8Threads, BF16 ? 3 : 2)
 fp8_quantize_weight_kernel(const void *__restrict__ w, int64_t ldw, int32_t N, int32_t K, int32_t kb,
                            uint8_t *__restrict__ wq, float *__restrict__ ws) {
+    using L = Fp8Lay<BF16>;
+    constexpr int P = 128 / L::BLOCKS;   // passes of BLOCKS rows
     pdl_launch_dependents();
     pdl_wait();
     __shared__ float part[kFp8Threads / 32];
     const int tid = threadIdx.x;
-    const int32_t kblk = blockIdx.x % kb, nblk = blockIdx.x / kb;
-    const int32_t col = kblk * 128 + 8 * (tid % kFp8Lanes), row0 = nblk * 128 + tid / kFp8Lanes;
-    Fp8In<BF16> in[8];
+    const int32_t nblk = blockIdx.x / kb, kblk = blockIdx.x - nblk * kb;
+    const int32_t col = kblk * 128 + 8 * L::NC * (tid % L::LANES);
+    const int64_t row0 = (int64_t)nblk * 128 + tid / L::LANES;
+    Fp8In<BF16> in[P];
 #pragma unroll
-    for (int p = 0; p < 8; ++p) in[p].load(w, (row0 + 16 * p) * ldw + col, row0 + 16 * p < N && col < K);
+    for (int p = 0; p < P; ++p)
+        in[p].template load<WIDE>(w, (row0 + L::BLOCKS * p) * ldw + col, row0 + L::BLOCKS * p < N && col < K);
     float m = 0.0f;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        f2_t v[4];
-        in[p].get(v);
-        m = fmaxf(m, amax_f2(v));
-    }
-    m = group16_max(m);
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int c = 0; c < L::NC; ++c) {
+            f2_t v[4];
+            in[p].get(c, v);
+            m = fmaxf(m, amax_f2(v));
+        }
+    m = block_max<32>(m);
     if (tid % 32 == 0) part[tid / 32] = m;
     __syncthreads();
 #pragma unroll
@@ -131,33 +168,35 @@ fp8_quantize_weight_kernel(const void *__restrict__ w, int64_t ldw, int32_t N, i
     const float s = fp8_block_scale(m, r);
     if (tid == 0) ws[blockIdx.x] = s;
 #pragma unroll
-    for (int p = 0; p < 8; ++p) {
-        if (row0 + 16 * p >= N || col >= K) continue;
-        f2_t v[4];
-        in[p].get(v);
-        *reinterpret_cast<uint2 *>(wq + (int64_t)(row0 + 16 * p) * K + col) = pack8_f2(v, r);
+    for (int p = 0; p < P; ++p) {
+        if (row0 + L::BLOCKS * p >= N || col >= K) continue;
+        f2_t v[L::NC][4];
+#pragma unroll
+        for (int c = 0; c < L::NC; ++c) in[p].get(c, v[c]);
+        store_codes<L::NC>(wq + (row0 + L::BLOCKS * p) * K + col, v, r);
     }
 }
 
 // The gated tail ("Red Lite dev15d - DeltaNet gated tail", Pinned graph semantics, steps 1-5) into FP8:
-// a block of 128 columns is 128 / D heads, each normalised over its own D / 8 lanes (gated_row8, the
-// plain tail's arithmetic), then one maximum and one scale over the 16 lanes. The codes come from the
-// fp32 values, with no rounding to bf16 between: the same bytes as the plain tail with an fp32 output
-// followed by fp8_quantize_act.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kFp8Threads)
+// a block of 128 columns is 128 / D heads, each normalised over its own lanes, then one maximum and one scale
+// over the block's. The codes come from the fp32 values, with no rounding to bf16 between: the same bytes as the
+// plain tail with an fp32 output followed by fp8_quantize_act. (The plain tail has 8 values a lane and adds its
+// lanes' squares from the farthest to the nearest; where a lane has two chunks here, they are the nearest.)
+template <int D, bool BF16, bool WIDE, int U>
+__global__ void __launch_bounds__(kFp8Threads, U == 1 ? 4 : BF16 ? 2 : 4)
 gated_rmsnorm_fp8_kernel(const void *__restrict__ o, const void *__restrict__ z, const float *__restrict__ w,
                          float eps, int32_t nblocks, int32_t kb, int32_t K, uint8_t *__restrict__ xq,
                          float *__restrict__ xs) {
+    using L = Fp8Lay<BF16>;
+    constexpr int NC = L::NC;
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int U = kFp8Unroll;
-    const int l = threadIdx.x % kFp8Lanes, wcol = 8 * l % D;
-    f2_t w2[4];
+    const int l = threadIdx.x % L::LANES, wcol = 8 * NC * l % D;
+    f2_t w2[NC][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w2[k] = f2(w[wcol + 2 * k], w[wcol + 2 * k + 1]);
-    const int64_t stride = (int64_t)gridDim.x * kFp8Blocks;
-    const int64_t first = (int64_t)blockIdx.x * kFp8Blocks;
+    for (int k = 0; k < 4 * NC; ++k) w2[k / 4][k % 4] = f2(w[wcol + 2 * k], w[wcol + 2 * k + 1]);
+    const int64_t stride = (int64_t)gridDim.x * L::BLOCKS;
+    const int64_t first = (int64_t)blockIdx.x * L::BLOCKS;
     for (int64_t i0 = first; i0 < nblocks; i0 += U * stride) {   // uniform over the CTA
         Fp8In<BF16> ro[U], rz[U];
         int32_t blk[U];
@@ -165,72 +204,101 @@ gated_rmsnorm_fp8_kernel(const void *__restrict__ o, const void *__restrict__ z,
         bool live[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + u * stride + threadIdx.x / kFp8Lanes;
+            const int64_t i = i0 + u * stride + threadIdx.x / L::LANES;
             blk[u] = (int32_t)min(i, (int64_t)nblocks - 1);
-            const int32_t row = blk[u] / kb, col = (blk[u] - row * kb) * 128 + 8 * l;
+            const int32_t row = blk[u] / kb, col = (blk[u] - row * kb) * 128 + 8 * NC * l;
             off[u] = (int64_t)row * K + col;
             live[u] = i < nblocks && col < K;
-            ro[u].load(o, off[u], live[u]);
-            rz[u].load(z, off[u], live[u]);
+            ro[u].template load<WIDE>(o, off[u], live[u]);
+            rz[u].template load<WIDE>(z, off[u], live[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            f2_t o2[4], z2[4], y2[4];
-            ro[u].get(o2);
-            rz[u].get(z2);
-            gated_row8<D / 8>(o2, z2, w2, 1.0f / (float)D, eps, y2);
-            float r;
-            const float s = fp8_block_scale(group16_max(live[u] ? amax_f2(y2) : 0.0f), r);
+            f2_t o2[NC][4], z2[4], y2[NC][4];
+            float sq[NC], m = 0.0f, r;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                ro[u].get(c, o2[c]);
+                sq[c] = row_sumsq8(o2[c]);
+            }
+#pragma unroll
+            for (int n = D / 16 / NC; n > 0; n >>= 1)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) sq[c] += __shfl_xor_sync(0xffffffffu, sq[c], n);
+            const float inv_rms = rsqrtf(__fmaf_rn(NC == 2 ? sq[0] + sq[NC - 1] : sq[0], 1.0f / (float)D, eps));
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                rz[u].get(c, z2);
+                gated_apply8(o2[c], z2, w2[c], inv_rms, y2[c]);
+            }
+            const float s = fp8_block_scale(block_max<L::LANES>(live[u] ? (NC == 2 ? fmaxf(amax_f2(y2[0]), amax_f2(y2[NC - 1])) : amax_f2(y2[0])) : 0.0f), r);
             if (!live[u]) continue;
-            *reinterpret_cast<uint2 *>(xq + off[u]) = pack8_f2(y2, r);
+            store_codes<NC>(xq + off[u], y2, r);
             if (l == 0) xs[blk[u]] = s;
         }
     }
 }
 
+// As many CTAs as there are passes, up to eight an SM.
+template <bool BF16>
 unsigned fp8_grid(int64_t nblocks) {
-    const int64_t per = (int64_t)kFp8Blocks * kFp8Unroll;
-    const int64_t want = (nblocks + per - 1) / per, cap = 148 * 8;
+    const int64_t want = (nblocks + Fp8Lay<BF16>::BLOCKS - 1) / Fp8Lay<BF16>::BLOCKS, cap = 148 * 8;
     return (unsigned)(want < cap ? want : cap);
+}
+// Long: more than one turn of one block a thread on the largest grid.
+template <bool BF16>
+bool fp8_long(int64_t nblocks) {
+    return nblocks > 148 * 8 * Fp8Lay<BF16>::BLOCKS;
+}
+
+bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+template <int D, bool BF16, bool WIDE>
+cudaError_t launch_tail_t(const Fp8TailArgs &t, cudaStream_t st) {
+    const int32_t K = t.Hv * t.D, kb = (K + 127) / 128, nblocks = t.M * kb;
+    // (fp32: two blocks a thread hold as many bytes, and four spill)
+    if (fp8_long<BF16>(nblocks))
+        return launch_pdl(gated_rmsnorm_fp8_kernel<D, BF16, WIDE, BF16 ? kFp8Long : 2>, dim3(fp8_grid<BF16>(nblocks)), dim3(kFp8Threads),
+                          0, st, t.o, t.z, t.w, t.eps, nblocks, kb, K, t.xq, t.xs);
+    return launch_pdl(gated_rmsnorm_fp8_kernel<D, BF16, WIDE, 1>, dim3(fp8_grid<BF16>(nblocks)), dim3(kFp8Threads), 0, st, t.o, t.z,
+                      t.w, t.eps, nblocks, kb, K, t.xq, t.xs);
 }
 
 template <int D>
-cudaError_t launch_tail_fp8_d(const Fp8TailArgs &t, int32_t kb, cudaStream_t st) {
-    const int32_t nblocks = t.M * kb, K = t.Hv * t.D;
-    if (t.in_bf16)
-        return launch_pdl(gated_rmsnorm_fp8_kernel<D, true>, dim3(fp8_grid(nblocks)), dim3(kFp8Threads), 0, st, t.o, t.z,
-                          t.w, t.eps, nblocks, kb, K, t.xq, t.xs);
-    return launch_pdl(gated_rmsnorm_fp8_kernel<D, false>, dim3(fp8_grid(nblocks)), dim3(kFp8Threads), 0, st, t.o, t.z,
-                      t.w, t.eps, nblocks, kb, K, t.xq, t.xs);
+cudaError_t launch_tail_d(const Fp8TailArgs &t, cudaStream_t st) {
+    const bool wide = aligned32(t.o) && aligned32(t.z);   // rows are multiples of 16 values
+    if (t.in_bf16) return wide ? launch_tail_t<D, true, true>(t, st) : launch_tail_t<D, true, false>(t, st);
+    return wide ? launch_tail_t<D, false, true>(t, st) : launch_tail_t<D, false, false>(t, st);
+}
+
+template <bool BF16, bool WIDE>
+cudaError_t launch_quantize_t(const Fp8QuantArgs &a, cudaStream_t st) {
+    const int32_t kb = (a.K + 127) / 128;
+    if (a.weight)
+        return launch_pdl(fp8_quantize_weight_kernel<BF16, WIDE>, dim3((unsigned)(kb * ((a.rows + 127) / 128))), dim3(kFp8Threads), 0,
+                          st, a.x, a.ldx, a.rows, a.K, kb, a.xq, a.xs);
+    const int32_t nblocks = a.rows * kb;
+    if (fp8_long<BF16>(nblocks))
+        return launch_pdl(fp8_quantize_act_kernel<BF16, WIDE, kFp8Long>, dim3(fp8_grid<BF16>(nblocks)), dim3(kFp8Threads), 0, st, a.x,
+                          a.ldx, nblocks, kb, a.K, a.xq, a.xs);
+    return launch_pdl(fp8_quantize_act_kernel<BF16, WIDE, 1>, dim3(fp8_grid<BF16>(nblocks)), dim3(kFp8Threads), 0, st, a.x, a.ldx,
+                      nblocks, kb, a.K, a.xq, a.xs);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_quantize(const Fp8QuantArgs &a, cudaStream_t st) {
-    const int32_t kb = (a.K + 127) / 128;
-    if (a.weight) {
-        const dim3 grid((unsigned)(kb * ((a.rows + 127) / 128)));
-        if (a.in_bf16)
-            return launch_pdl(fp8_quantize_weight_kernel<true>, grid, dim3(kFp8Threads), 0, st, a.x, a.ldx, a.rows, a.K, kb,
-                              a.xq, a.xs);
-        return launch_pdl(fp8_quantize_weight_kernel<false>, grid, dim3(kFp8Threads), 0, st, a.x, a.ldx, a.rows, a.K, kb,
-                          a.xq, a.xs);
-    }
-    const int32_t nblocks = a.rows * kb;
-    if (a.in_bf16)
-        return launch_pdl(fp8_quantize_act_kernel<true>, dim3(fp8_grid(nblocks)), dim3(kFp8Threads), 0, st, a.x, a.ldx,
-                          nblocks, kb, a.K, a.xq, a.xs);
-    return launch_pdl(fp8_quantize_act_kernel<false>, dim3(fp8_grid(nblocks)), dim3(kFp8Threads), 0, st, a.x, a.ldx,
-                      nblocks, kb, a.K, a.xq, a.xs);
+    const bool wide = aligned32(a.x) && a.ldx % (a.in_bf16 ? 16 : 8) == 0;   // every row starts on 32 bytes
+    if (a.in_bf16) return wide ? launch_quantize_t<true, true>(a, st) : launch_quantize_t<true, false>(a, st);
+    return wide ? launch_quantize_t<false, true>(a, st) : launch_quantize_t<false, false>(a, st);
 }
 
 cudaError_t launch_gated_rmsnorm_fp8(const Fp8TailArgs &t, cudaStream_t st) {
-    const int32_t kb = (t.Hv * t.D + 127) / 128;
     switch (t.D) {
-        case 16: return launch_tail_fp8_d<16>(t, kb, st);
-        case 32: return launch_tail_fp8_d<32>(t, kb, st);
-        case 64: return launch_tail_fp8_d<64>(t, kb, st);
-        case 128: return launch_tail_fp8_d<128>(t, kb, st);
+        case 16: return launch_tail_d<16>(t, st);
+        case 32: return launch_tail_d<32>(t, st);
+        case 64: return launch_tail_d<64>(t, st);
+        case 128: return launch_tail_d<128>(t, st);
         default: return cudaErrorInvalidValue;
     }
 }
