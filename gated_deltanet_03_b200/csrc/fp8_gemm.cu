@@ -7,24 +7,31 @@
 //
 // fp8_gemm_narrow_kernel: the weight takes the MMA's M side (a tile of 128 rows of b on the 128 tensor-memory
 // lanes), MT activation rows (16, 32, 64 or 128) the N side, so that few tokens cost no more MMA or
-// tensor-memory work than they need. K is split over a cluster of CTAs along grid z where the tiles
-// alone would leave SMs idle; the partial sums are written into the shared memory of the CTA that stores them, which adds them in rank order.
+// tensor-memory work than they need. K is split over a cluster of CTAs along grid z where the tiles alone would
+// leave SMs idle; the partial sums are written into the shared memory of the CTA that stores them, which adds them in
+// rank order, so results do not depend on scheduling. One K block takes an SM 510 cycles at MT = 16 (waits, four MMAs and
+// their commits one after another in one warp) to 870 at MT = 128.
 //   warp 0     TMA producer: weight tile (128 rows x 128 B) and activation tile (MT x 128 B) per K block;
-//   warp 1     tensor memory and the MMA issue (one thread);
+//   warp 1     tensor memory and the MMA issue;
 //   warps 2-3  the factors as[m, B] bs[n0 / 128, B] of the tile's MT rows, eight K blocks at a time;
 //   warps 4-   one weight row and 32 of the MT columns per thread (16 for MT = 16): accumulator -> registers, one
 //              FMA per value, and at the end the tile through shared memory to y.
 //
-// fp8_gemm_wide_kernel, for many tokens: SM pairs (tcgen05.mma.cta_group::2) on 256 x 256 tiles, tokens on the M
-// side, CTA r of a pair holding 128 token rows and half of the 256 weight rows, so that a K block costs each SM
-// 32 KB of loads for 512 cycles of MMA (a 128 x 128 tile on one SM: 32 KB for 256, and loads are what
-// bounds it). Persistent; the two accumulators take all of tensor memory, so that the MMAs of one K block
-// run while the block before is scaled and added by the eight promotion warps, 128 fp32 sums a thread
-// (register split by setmaxnreg: 128 x 72 + 256 x 216 = 384 x 168, the launch's own total).
-//   warp 0     TMA producer of this CTA's operands;   warp 1     (leader) MMA issue;
+// fp8_gemm_wide_kernel, for many tokens: SM pairs (tcgen05.mma.cta_group::2) on tiles of 256 tokens x BN columns (128,
+// 192 or 256), tokens on the M side, CTA r of a pair holding 128 token rows and half of the BN weight rows, so that a K
+// block of a 256-wide tile costs each SM 32 KB of loads for 512 cycles of MMA. Persistent, the pairs walking the tiles
+// along N first; the accumulators (two, or four of 128 columns) fill tensor memory, so that the MMAs of one K block run
+// while the one before is scaled and added.
+//   warp 0     TMA producer of this CTA's operands;
+//   warp 1     (leader) MMA issue;
 //   warp 2     (peer) tells the leader that a stage's operands have landed here;
-//   warp 3     the factors as[m, B] bs[n / 128, B] of this CTA's rows, through shared memory;
-//   warps 4-11 one token row and half of the 256 columns per thread.
+//   warp 3     the factors as[m, B] bs[n / 128, B], through shared memory;
+//   warps 4-   (BN / 16 promotion warps) one token row and 64 columns per thread, in fp32 registers (at BN = 256 the
+//              register split by setmaxnreg is 128 x 64 + 512 x 104 = 640 x 96, the launch's own total).
+// A K block of a 256-wide tile takes 840 cycles: the MMAs alone 512, with their signals and loads 620, and the read-back,
+// which shares tensor memory with them, the rest (reading 128 x 256 sums flat out slows a group of MMAs by 28 %).
+// 32768 x 2048 x 4096: 257 us in a burst (2.14 PFLOP/s), 290 to 300 us back to back, where the 1 kW limit holds the SMs at
+// 1.5 GHz.
 //
 // Every barrier wait is bounded (gdn_debug_set_wait); an expired one records GDN_ERR_TIMEOUT, issued copies
 // and MMAs are waited for (bounded), tensor memory is freed and the CTA ends.
@@ -36,6 +43,10 @@ namespace {
 
 constexpr int kChunk = 8;                  // K blocks per set of staged factors
 constexpr int kMaxSplit = 8;
+// Stages loaded before the CTAs of a pair meet: from the producer's loop the first load left 1,600 cycles later (256 x
+// 12352 x 2048 in 11.4 us, now 11.0); but a stage takes 300 cycles to issue, and with all of them first the rest of
+// the pair waited for that.
+constexpr int kEarly = 2;
 
 template <int MT>
 struct NarrowCfg {
@@ -418,6 +429,29 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         tma_prefetch_desc(&map_a);
         tma_prefetch_desc(&map_b);
     }
+    // The producer's place: tile pt, K block pk of it, stage ps. Its first loads go out before the CTAs of the pair meet
+    // (they touch this CTA's barriers alone).
+    int pt = pair, pk = 0, pit = 0, ps = 0, pm = pair / tiles_n * 256 + rank * 128, pn = pair % tiles_n * BN + rank * (BN / 2);
+    auto load_stage = [&] {
+        if (f8_elect()) {
+            mbar_arrive_expect_tx(&full[ps], Cfg::STAGE_BYTES);
+            tma_load_2d(tile_a(ps), &map_a, &full[ps], pk * 128, pm);
+            tma_load_2d(tile_b(ps), &map_b, &full[ps], pk * 128, pn);
+        }
+        ++pit;
+        if (++pk == num_k) {
+            pk = 0;
+            pt += npairs;
+            pm = pt / tiles_n * 256 + rank * 128;
+            pn = pt % tiles_n * BN + rank * (BN / 2);
+        }
+        if (++ps == STAGES) ps = 0;
+    };
+    if (warp == 0) {
+        __syncwarp();
+        pdl_wait();
+        while (pit < kEarly && pit < total) load_stage();
+    }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512)
                      : "memory");
@@ -432,27 +466,13 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     if (warp < 4) {
         if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 0) {
-            int it = 0, s = 0;
-            uint32_t ph = 1;
-            bool ok = true;
-            for (int t = pair; t < num_tiles && ok; t += npairs) {
-                const int m0 = t / tiles_n * 256 + rank * 128, n0 = t % tiles_n * BN + rank * (BN / 2);
-                for (int k = 0; k < num_k; ++k, ++it) {
-                    if (!(ok = f8_warp_wait(&empty[s], ph, status))) break;
-                    if (f8_elect()) {
-                        mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
-                        tma_load_2d(tile_a(s), &map_a, &full[s], k * 128, m0);
-                        tma_load_2d(tile_b(s), &map_b, &full[s], k * 128, n0);
-                    }
-                    if (++s == STAGES) {
-                        s = 0;
-                        ph ^= 1;
-                    }
-                }
+            for (; pit < total;) {
+                if (!f8_warp_wait(&empty[ps], (uint32_t)(((pit / STAGES) & 1) ^ 1), status)) break;
+                load_stage();
             }
             // before the CTA may exit: the latest load armed on each stage has landed
-            for (int s = 0; s < STAGES && s < it; ++s) {
-                const int last = it - 1 - ((it - 1 - s) % STAGES);
+            for (int s = 0; s < STAGES && s < pit; ++s) {
+                const int last = pit - 1 - ((pit - 1 - s) % STAGES);
                 mbar_wait(&full[s], (uint32_t)((last / STAGES) & 1), status);
             }
         } else if (warp == 1 && rank == 0) {
@@ -623,9 +643,11 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         }
     }
 
-    // neither CTA frees tensor memory or exits while the pair's MMAs, reads or arrivals may touch it
+    // Neither CTA frees tensor memory or exits while the pair's MMAs, reads or arrivals may touch it. Relaxed: no data of
+    // the other CTA is read after it, and a release would wait for the stores of y to be performed.
     tc_fence_before();
-    f8_cluster_sync();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    f8_cluster_wait();
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
