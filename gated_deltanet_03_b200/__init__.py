@@ -518,9 +518,19 @@ def gdn_short_conv1d_silu_decode(x, weight, conv_state, parts=None, y=None, stre
 
 # ---------------------------------------------------- FP8 and pooled decode ----
 # These calls run on the device of their tensors, whichever device is current, and outputs that they
-# allocate belong to the stream that writes them. They are made once per layer and token, where a call's
-# time on the host is longer than its kernel: each checks its tensors in one pass (_ok) and goes
-# through the named checks above only to say what is wrong.
+# allocate belong to the stream that writes them. They are made once per layer and token, where a call's time on
+# the host is longer than its kernel's: a plainly right call on the current device and stream is checked and made by
+# csrc/host.cpp (3 us against 6 to 13 from here for the calls of a decode step); all others, and all where that is not
+# built, are made from here, each checking its tensors in one pass (_ok) and going through the named checks above
+# only to say what is wrong.
+
+try:
+    from . import _gdn_host as _host
+    _host.bind(*[ctypes.cast(getattr(LIB, n), ctypes.c_void_p).value for n in (
+        "fp8_gemm", "fp8_quantize_act", "fp8_quantize_weight", "gdn_gated_rmsnorm_silu_fp8", "gdn_decode_step_pooled",
+        "gdn_decode_step_pooled_gated_fp8", "gdn_short_conv1d_silu_decode_pooled")])
+except ImportError:
+    _host = None
 
 _F8, _BF = (torch.float8_e4m3fn,), (torch.bfloat16,)
 _f8, _bf, _f32, _i32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
@@ -594,17 +604,29 @@ def _fp8_quantize(fn, x, xq, xs, per_row, stream):
 def fp8_quantize_act(x, xq=None, xs=None, stream=None):
     """x [M, K] bf16/fp32 (rows may be strided) -> (xq [M, K] float8_e4m3fn, xs [M, ceil(K/128)] fp32),
     one scale per 128 values of a row. K % 16 == 0."""
+    if _host is not None and stream is None:
+        r = _host.fp8_quantize(x, xq, xs, False)
+        if r is not None:
+            return r
     return _fp8_quantize(LIB.fp8_quantize_act, x, xq, xs, True, stream)
 
 
 def fp8_quantize_weight(w, wq=None, ws=None, stream=None):
     """w [N, K] bf16/fp32 (rows may be strided) -> (wq [N, K] float8_e4m3fn, ws [ceil(N/128), ceil(K/128)] fp32),
     one scale per 128 x 128 block. K % 16 == 0."""
+    if _host is not None and stream is None:
+        r = _host.fp8_quantize(w, wq, ws, True)
+        if r is not None:
+            return r
     return _fp8_quantize(LIB.fp8_quantize_weight, w, wq, ws, False, stream)
 
 
 def fp8_gemm(aq, as_, bq, bs, out_dtype=torch.bfloat16, y=None, stream=None):
     """(aq [M, K], as [M, ceil(K/128)]) x (bq [N, K], bs [ceil(N/128), ceil(K/128)])^T -> y [M, N]."""
+    if _host is not None and stream is None and (y is not None or out_dtype is _bf or out_dtype is _f32):
+        r = _host.fp8_gemm(aq, as_, bq, bs, y, out_dtype is _f32)
+        if r is not None:
+            return r
     M, K = aq.shape
     N, Kb = bq.shape
     kb = (K + 127) // 128
@@ -624,6 +646,10 @@ def fp8_gemm(aq, as_, bq, bs, out_dtype=torch.bfloat16, y=None, stream=None):
 
 def gdn_gated_rmsnorm_silu_fp8(o, z, weight, eps: float = 1e-6, xq=None, xs=None, stream=None):
     """o, z [M, Hv, D] -> (xq [M, Hv * D] float8_e4m3fn, xs [M, ceil(Hv * D / 128)] fp32)."""
+    if _host is not None and stream is None:
+        r = _host.tail(o, z, weight, eps, xq, xs)
+        if r is not None:
+            return r
     M, Hv, D = o.shape
     K = Hv * D
     kb = (K + 127) // 128
@@ -669,6 +695,10 @@ def gdn_decode_step_pooled(q, k, v, a, b, A_log, dt_bias, state_pool, slots, sca
     """gdn_decode_step on states in a pool: row i uses slot slots[i] (device int32 [B]) of state_pool
     [num_slots, Hv, 128, 128] fp32, in place; a negative slot marks a padded row, whose state and output
     stay as they are (a new output is zero there). a, b [B, Hv] bf16 or fp32, rows may be strided. Returns o."""
+    if _host is not None and stream is None and (out_dtype is None or out_dtype is _bf or out_dtype is _f32):
+        r = _host.decode(q, k, v, a, b, A_log, dt_bias, state_pool, slots, scale, qk_l2norm, o, out_dtype is _f32)
+        if r is not None:
+            return r
     dev, B, Hk, Hv, ldg = _pooled_sizes(q, k, v, a, b, A_log, dt_bias, state_pool, slots)
     D = q.shape[2]
     if o is None:
@@ -688,6 +718,10 @@ def gdn_decode_step_pooled_gated_fp8(q, k, v, a, b, A_log, dt_bias, state_pool, 
     """gdn_decode_step_pooled with the gated RMSNorm and its FP8 encode fused: z [B, Hv, 128] bf16 (rows may
     be strided), norm_weight [128] fp32. Returns (xq [B, Hv*128] float8_e4m3fn, xs [B, Hv] fp32, o or None);
     o (bf16) is written only when given. New outputs are zero in padded rows."""
+    if _host is not None and stream is None:
+        r = _host.decode(q, k, v, a, b, A_log, dt_bias, state_pool, slots, scale, qk_l2norm, o, z, norm_weight, eps, xq, xs)
+        if r is not None:
+            return r
     dev, B, Hk, Hv, ldg = _pooled_sizes(q, k, v, a, b, A_log, dt_bias, state_pool, slots)
     if z is None or norm_weight is None:
         raise ValueError("z and norm_weight are required")
@@ -714,6 +748,10 @@ def gdn_decode_step_pooled_gated_fp8(q, k, v, a, b, A_log, dt_bias, state_pool, 
 def gdn_short_conv1d_silu_decode_pooled(x, weight, conv_pool, slots, parts=None, y=None, stream=None):
     """gdn_short_conv1d_silu_decode on a pool: row i shifts slot slots[i] (device int32 [B], negative: a
     padded row, left as it is; a new y is zero there) of conv_pool bf16 [num_slots, K - 1, C] in place."""
+    if _host is not None and stream is None:
+        r = _host.conv(x, weight, conv_pool, slots, parts, y)
+        if r is not None:
+            return r
     B, C, ldx = _conv_rows(x)
     K = weight.shape[1]
     if conv_pool is None or slots is None:

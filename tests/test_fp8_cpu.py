@@ -152,3 +152,16 @@ def test_fp8_binding_refusals():
         g.gdn_short_conv1d_silu_decode_pooled(x, torch.zeros(64, 4), torch.zeros(5, 4, 64, dtype=BF), torch.zeros(4, dtype=torch.int32))
     with pytest.raises(ValueError, match="required"):
         g.gdn_short_conv1d_silu_decode_pooled(x, torch.zeros(64, 4), None, torch.zeros(4, dtype=torch.int32))
+
+
+def test_host_path_is_built_and_declines_quietly():
+    """The compiled host path is there; what it does not take it answers with None, whatever it is given."""
+    assert g._host is not None
+    x = torch.zeros(4, 64, dtype=BF)
+    odd = [(), (1,), (None,) * 6, (x,) * 4, (x, None, None, False), ("a", 2.0, None, x, x, 1), (x,) * 6, (x,) * 13, (x,) * 17,
+           (x, x, x, x, (64, "b"), None), (None,) * 17]
+    for f in (g._host.fp8_gemm, g._host.fp8_quantize, g._host.tail, g._host.decode, g._host.conv):
+        for args in odd:
+            assert f(*args) is None
+    with pytest.raises(TypeError):
+        g._host.bind(1, 2)

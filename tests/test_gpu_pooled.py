@@ -13,13 +13,18 @@ pytestmark = pytest.mark.gpu
 F8, BF, F32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32
 
 
-@pytest.fixture(scope="module")
-def g():
+@pytest.fixture(scope="module", params=["host", "ctypes"])
+def g(request):
+    """The library with its calls made by the compiled host path, and through ctypes alone."""
     if not torch.cuda.is_available():
         pytest.skip("no GPU")
     import gated_deltanet_03_b200 as lib
     lib.gdn_get_device_status()
+    host = lib._host
+    assert host is not None
+    lib._host = host if request.param == "host" else None
     yield lib
+    lib._host = host
     assert lib.gdn_get_device_status() == 0
 
 
