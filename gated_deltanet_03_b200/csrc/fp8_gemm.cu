@@ -9,7 +9,9 @@
 // lanes), MT activation rows (16, 32, 64 or 128) the N side, so that few tokens cost no more MMA or
 // tensor-memory work than they need. K is split over a cluster of CTAs along grid z where the tiles alone would
 // leave SMs idle; the partial sums are written into the shared memory of the CTA that stores them, which adds them in
-// rank order, so results do not depend on scheduling. One K block takes an SM 510 cycles at MT = 16 (waits, four MMAs and
+// rank order, so results do not depend on scheduling. They have a place of their own there, so that nothing waits for
+// another CTA's loads and MMAs (over the idle stage ring, behind a cluster barrier, the exchange took half of the 5.0 us
+// of 1 x 2048 x 4096, which now takes 4.1 to 4.4). One K block takes an SM 510 cycles at MT = 16 (waits, four MMAs and
 // their commits one after another in one warp) to 870 at MT = 128.
 //   warp 0     TMA producer: weight tile (128 rows x 128 B) and activation tile (MT x 128 B) per K block;
 //   warp 1     tensor memory and the MMA issue;
@@ -50,24 +52,34 @@ constexpr int kEarly = 2;
 
 template <int MT>
 struct NarrowCfg {
-    // Two CTAs an SM for the narrow tiles, whose K splits then reach further: 1 x 2048 x 4096 takes 4.8 us in eight
-    // ranges, 5.1 in four with one CTA an SM and twice the stages.
+    // Two CTAs an SM for the narrow tiles, so that as many clusters of eight run at once as their K splits need: 16 x
+    // 2048 x 4096 takes 4.5 us in eight ranges, 5.2 in four.
     static constexpr int CTAS = MT <= 32 ? 2 : 1;
-    static constexpr int STAGES = MT == 16 ? 6 : MT == 32 ? 5 : MT == 64 ? 9 : 6;
+    static constexpr int STAGES = MT == 16 ? 5 : MT == 32 ? 4 : MT == 64 ? 7 : 4;
     static constexpr int W_BYTES = 128 * 128, X_BYTES = MT * 128;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
     static constexpr int COLS = MT == 16 ? 16 : 32;            // accumulator columns per thread, one tensor-memory load
     static constexpr int EPI_WARPS = 4 * MT / COLS;
     static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-    static constexpr int PITCH = 132;                          // fp32 pitch of a column of the partial sums
-    static constexpr int OFF_SCL = STAGES * STAGE_BYTES;
+    static constexpr int PITCH = 132;                          // unsplit: fp32 pitch of a column of the tile, over the stage ring
+    static constexpr int OFF_PART = STAGES * STAGE_BYTES;      // split: the partial sums of this CTA's columns
+    // fp32 pitch of a weight row in a CTA's share of c columns (padded off the bank stride), and all shares' size
+    static constexpr int part_pitch(int c) { return c <= 4 ? c : c + 4; }
+    static constexpr int part_bytes(int split) { return split * 128 * part_pitch(MT / split) * 4; }
+    // Narrow tiles send with st.async and wait for the bytes (1 x 2048 x 4096 in 4.1 us, 4.3 with plain stores and a second
+    // cluster barrier); the wider tiles' many sums go faster as plain stores (128 x 2048 x 4096 in 7.9 us, 8.5 by st.async).
+    static constexpr bool ASYNC = MT <= 32;
+    static constexpr int larger(int a, int b) { return a > b ? a : b; }
+    static constexpr int PART_BYTES = larger(part_bytes(2), larger(part_bytes(4), part_bytes(8)));
+    static constexpr int OFF_SCL = OFF_PART + PART_BYTES;
     static constexpr int OFF_BAR = OFF_SCL + 2 * kChunk * MT * 4;
     static constexpr int SMEM = OFF_BAR + 512 + 1024;
     static constexpr int TMEM_COLS = 2 * MT;
-    static_assert(MT * PITCH * 4 <= STAGES * STAGE_BYTES, "the partial sums fit over the stage ring");
+    static_assert(MT * PITCH * 4 <= STAGES * STAGE_BYTES, "the tile fits over the stage ring");
+    static_assert(PART_BYTES >= part_bytes(2) && PART_BYTES >= part_bytes(4) && PART_BYTES >= part_bytes(8), "every split's shares fit");
     static_assert(STAGE_BYTES % 1024 == 0, "stage bases stay 1024-byte aligned");
     static_assert(MT % kMaxSplit == 0, "whole columns for every CTA of a cluster");
-    static_assert(SMEM <= 232448 && CTAS * (SMEM + 1024) <= 233472 && 8 * (2 * STAGES + 9) + 4 <= 512, "layout");
+    static_assert(SMEM <= 232448 && CTAS * (SMEM + 1024) <= 233472 && 8 * (2 * STAGES + 10) + 4 <= 512, "layout");
 };
 
 __device__ __forceinline__ uint32_t f8_cluster_rank() {
@@ -87,8 +99,21 @@ __device__ __forceinline__ uint32_t f8_mapa(const void *p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void f8_st_cluster(uint32_t at, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+// V values into another CTA's shared memory; with ASYNC their bytes complete on a barrier there.
+template <int V, bool ASYNC>
+__device__ __forceinline__ void f8_st_cluster(uint32_t at, const float *v, uint32_t bar) {
+    if constexpr (ASYNC && V == 4)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at), "f"(v[0]),
+                     "f"(v[1]), "f"(v[2]), "f"(v[3]), "r"(bar)
+                     : "memory");
+    else if constexpr (ASYNC)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at), "f"(v[0]), "f"(v[1]),
+                     "r"(bar)
+                     : "memory");
+    else if constexpr (V == 4)
+        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+    else
+        asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v[0]), "f"(v[1]) : "memory");
 }
 __device__ __forceinline__ void f8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
@@ -142,6 +167,50 @@ __device__ __forceinline__ void store_y4(void *y, int64_t idx, float4 v) {
     }
 }
 
+// This thread's sums (one weight row, COLS columns from its group's first) to the CTAs that store them: columns
+// [r cpr, (r + 1) cpr) of the tile to CTA r, into the share of this CTA there, [weight row][column].
+template <int MT, int V>
+__device__ __forceinline__ void f8_send_parts(uint8_t *sm, uint64_t *parts, const float (&acc)[NarrowCfg<MT>::COLS], int warp, int lane,
+                                              int crank, int cpr) {
+    using Cfg = NarrowCfg<MT>;
+    const int c0 = ((warp - 4) >> 2) * Cfg::COLS, row = (warp & 3) * 32 + lane, pitch = Cfg::part_pitch(cpr), sh = __ffs(cpr) - 1;
+    const float *share = reinterpret_cast<const float *>(sm + Cfg::OFF_PART) + (crank * 128 + row) * pitch;
+#pragma unroll
+    for (int c = 0; c < Cfg::COLS; c += V) {
+        const uint32_t to = (uint32_t)((c0 + c) >> sh);   // cpr is a power of two
+        f8_st_cluster<V, Cfg::ASYNC>(f8_mapa(share + ((c0 + c) & (cpr - 1)), to), acc + c, f8_mapa(parts, to));
+    }
+}
+
+// The shares of this CTA's cpr columns (activation rows m_first ..), added in rank order and stored.
+template <int MT, int V, bool OUT_BF16>
+__device__ __forceinline__ void f8_sum_parts(const uint8_t *sm, void *y, int tid, int m_first, int n0, int M, int N, int split, int cpr) {
+    using Cfg = NarrowCfg<MT>;
+    const int pitch = Cfg::part_pitch(cpr);
+    for (int u = tid; u < 128 * (cpr / V); u += Cfg::THREADS) {
+        const int row = u % 128, c = u / 128 * V;
+        const float *src = reinterpret_cast<const float *>(sm + Cfg::OFF_PART) + row * pitch + c;
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.0f;
+#pragma unroll 8
+        for (int z = 0; z < split; ++z) {   // in rank order
+            const float *t = src + z * 128 * pitch;
+            if constexpr (V == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(t);
+                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(t);
+                v[0] += x.x; v[1] += x.y;
+            }
+        }
+        if (n0 + row >= N) continue;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (m_first + c + i < M) store1<OUT_BF16>(y, (size_t)(m_first + c + i) * N + n0 + row, v[i]);
+    }
+}
+
 template <int MT, bool OUT_BF16>
 __global__ void __launch_bounds__(NarrowCfg<MT>::THREADS, NarrowCfg<MT>::CTAS)
 fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -155,8 +224,8 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     float *scl = reinterpret_cast<float *>(sm + Cfg::OFF_SCL);            // [2][kChunk][MT]
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Cfg::OFF_BAR);
     uint64_t *full = bars, *empty = bars + STAGES, *acc_full = bars + 2 * STAGES, *acc_empty = acc_full + 2;
-    uint64_t *scl_full = acc_full + 4, *scl_empty = acc_full + 6, *drain = acc_full + 8;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 9);
+    uint64_t *scl_full = acc_full + 4, *scl_empty = acc_full + 6, *drain = acc_full + 8, *parts = acc_full + 9;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 10);
     auto tile_w = [&](int s) { return sm + s * Cfg::STAGE_BYTES; };
     auto tile_x = [&](int s) { return sm + s * Cfg::STAGE_BYTES + Cfg::W_BYTES; };
 
@@ -164,8 +233,9 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     const int n0 = blockIdx.x * 128, m0 = blockIdx.y * MT;
     // this CTA's K blocks: [kb0, kb0 + nkb), at least one (split <= kb_all)
     const int crank = split > 1 ? (int)f8_cluster_rank() : 0;
-    const int kb0 = (int)((int64_t)crank * kb_all / split);
-    const int nkb = (int)((int64_t)(crank + 1) * kb_all / split) - kb0;
+    const int split_log = __ffs(split) - 1;   // (a power of two)
+    const int kb0 = (int)((int64_t)crank * kb_all >> split_log);
+    const int nkb = (int)((int64_t)(crank + 1) * kb_all >> split_log) - kb0;
 
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -179,8 +249,13 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             mbar_init(&scl_empty[b], Cfg::EPI_WARPS);
         }
         mbar_init(drain, 1);
+        mbar_init(parts, 1);
         fence_barrier_init();
+        // the sums of this CTA's MT / split columns from every CTA of the cluster
+        if (Cfg::ASYNC && split > 1) mbar_arrive_expect_tx(parts, MT * 128 * 4);
     }
+    __syncwarp();
+    if (split > 1) f8_cluster_arrive();   // (below: nothing is sent to a CTA before it has come this far)
     if (warp == 1) {
         tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
         tmem_relinquish();
@@ -295,44 +370,38 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         }
         acc_ok = ok;
     }
-    // Every thread reaches the barriers, on the failure path too (the sums are then stale and the status word
-    // already says so). At the first one every CTA's stage ring is idle (its loads have landed and been read by
-    // MMAs that have completed); then the sums of column c (an activation row) go over the ring of CTA c / cpr,
-    // into its rows of this CTA's; after the second nothing is written to or read from another CTA.
     __syncwarp();
-    if (split > 1) f8_cluster_sync();
-    else __syncthreads();
-    const int cpr = MT / split;
-    if (acc_ok) {
-        const int quarter = warp & 3, group = (warp - 4) >> 2;
-        if (split == 1) {
-            float *part = reinterpret_cast<float *>(sm) + quarter * 32 + lane;
+    if (split == 1) {
+        // the tile over the idle stage ring (its loads have landed and been read by MMAs that have completed): column c
+        // (an activation row) at c * PITCH, weight rows consecutive
+        __syncthreads();
+        if (acc_ok) {
+            float *part = reinterpret_cast<float *>(sm) + (warp & 3) * 32 + lane;
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) part[(group * COLS + c) * Cfg::PITCH] = acc[c];
-        } else {
-#pragma unroll
-            for (int c = 0; c < COLS; ++c) {
-                const int col = group * COLS + c, to = col / cpr;
-                const float *part = reinterpret_cast<const float *>(sm) + (crank * cpr + col - to * cpr) * Cfg::PITCH;
-                f8_st_cluster(f8_mapa(part + quarter * 32 + lane, (uint32_t)to), acc[c]);
-            }
+            for (int c = 0; c < COLS; ++c) part[(((warp - 4) >> 2) * COLS + c) * Cfg::PITCH] = acc[c];
         }
-    }
-    if (split > 1) f8_cluster_sync();
-    else __syncthreads();
-    for (int u = tid; u < cpr * 32; u += Cfg::THREADS) {
-        const int c = crank * cpr + u / 32, j = 4 * (u % 32);
-        if (m0 + c >= M || n0 + j >= N) continue;
-        const float *src = reinterpret_cast<const float *>(sm) + (u / 32) * Cfg::PITCH + j;
-        float4 v = *reinterpret_cast<const float4 *>(src);
-        for (int z = 1; z < split; ++z) {   // in rank order
-            const float4 t = *reinterpret_cast<const float4 *>(src + z * cpr * Cfg::PITCH);
-            v.x += t.x;
-            v.y += t.y;
-            v.z += t.z;
-            v.w += t.w;
+        __syncthreads();
+        for (int u = tid; u < MT * 32; u += Cfg::THREADS) {
+            const int c = u / 32, j = 4 * (u % 32);
+            if (m0 + c < M && n0 + j < N)
+                store_y4<OUT_BF16>(y, (int64_t)(m0 + c) * N + n0 + j,
+                                   *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm) + c * Cfg::PITCH + j));
         }
-        store_y4<OUT_BF16>(y, (int64_t)(m0 + c) * N + n0 + j, v);
+    } else {
+        const int cpr = MT >> split_log;
+        f8_cluster_wait();
+        if (acc_ok) {
+            if (cpr >= 4) f8_send_parts<MT, 4>(sm, parts, acc, warp, lane, crank, cpr);
+            else f8_send_parts<MT, 2>(sm, parts, acc, warp, lane, crank, cpr);
+        }
+        __syncwarp();
+        f8_cluster_arrive();
+        bool here = true;   // the sums of every CTA of the cluster have arrived in this one
+        if constexpr (Cfg::ASYNC) here = f8_warp_wait(parts, 0, status);
+        else f8_cluster_wait();
+        if (here && cpr >= 4) f8_sum_parts<MT, 4, OUT_BF16>(sm, y, tid, m0 + crank * cpr, n0, M, N, split, cpr);
+        else if (here) f8_sum_parts<MT, 2, OUT_BF16>(sm, y, tid, m0 + crank * cpr, n0, M, N, split, cpr);
+        if constexpr (Cfg::ASYNC) f8_cluster_wait();   // no CTA ends while another may still send to it
     }
     tc_fence_before();
     __syncthreads();
@@ -796,10 +865,10 @@ cudaError_t launch_wide(const Fp8GemmArgs &g, int pairs, cudaStream_t st) {
 
 // The kernel and tile with the least estimated time: a start, and per wave of CTAs (or pairs) an end and a cost for
 // each K block, in us at 1965 MHz. Fitted to timings of each form at 1 to 64 K blocks (bf16 output, CUDA-graph
-// replay). Over 33 shapes of 1 to 32768 rows the pick was 1 % behind the fastest form on average, 12 % at
+// replay). Over 30 shapes of 1 to 22624 rows the pick was 2 % behind the fastest form on average, 11 % at
 // most; for example (us: narrow 64, narrow 128, wide 128, wide 192, wide 256)
-//     256 x 2048 x 4096   10.3, 12.4, 13.6, 16.0, 18.3      1024 x 2048 x 4096   25.8, 19.0, 15.1, 17.4, 19.3
-//     256 x 12352 x 2048  24.5, 21.9, 14.9, 11.6, 13.4      4096 x 1024 x 2048   30.7, 21.5, 15.4, 18.2, 13.1
+//     256 x 2048 x 4096   10.3, 13.4, 14.1, 16.6, 19.0      1024 x 2048 x 4096   27.1, 18.7, 15.2, 17.8, 20.0
+//     128 x 2048 x 4096    8.5, 10.8, 13.9, 16.6, 19.2      4096 x 1024 x 2048   30.7, 20.9, 15.9, 19.0, 13.6
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st) {
     Fp8Device dev;
     const cudaError_t e = f8_device(&dev);
@@ -809,8 +878,8 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st) {
         int tile;
         float start, end, block, push;   // push: what a split's exchange of partial sums adds
     };
-    static const Form narrow[4] = {{16, 2.1f, 1.0f, 0.26f, 0.8f}, {32, 2.2f, 1.0f, 0.285f, 1.4f}, {64, 2.7f, 1.0f, 0.31f, 2.3f},
-                                   {128, 3.6f, 1.0f, 0.42f, 3.6f}};
+    static const Form narrow[4] = {{16, 2.1f, 1.0f, 0.26f, 0.4f}, {32, 2.2f, 1.0f, 0.285f, 0.9f}, {64, 2.7f, 1.0f, 0.31f, 1.1f},
+                                   {128, 3.6f, 1.0f, 0.42f, 2.3f}};
     static const Form wide[3] = {{128, 3.2f, 0.8f, 0.311f, 0.0f}, {192, 3.8f, 1.0f, 0.381f, 0.0f}, {256, 4.2f, 1.2f, 0.4275f, 0.0f}};
     float best = 3.0e38f;
     int form = 0, split = 1;

@@ -7,7 +7,7 @@
 // HBM-bound: 128 KB of state traffic and about 8 operations a state value per (row, head) item. The grid has one
 // CTA per unit of one or more heads of a row; those that run take over the units of CTAs that have not been
 // launched yet (cluster launch control), so each SM does as many as its share of the memory rate allows (equal
-// shares left the fastest SMs idle for a fifth of the time: 188 us against KKK for 256 rows x 32 heads). A
+// shares left the fastest SMs idle for a fifth of the time: 188 us against 169 for 256 rows x 32 heads). A
 // producer warp brings each item's 64 KB state and its q, k, v, z rows into a ring by bulk copies, so loads
 // stay in flight while items are computed, written back and encoded:
 //   warps 0-15   the state from the stage into registers (8 lanes a row, 2 rows a thread, in the arithmetic of
