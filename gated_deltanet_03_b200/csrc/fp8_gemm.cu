@@ -866,7 +866,9 @@ cudaError_t launch_wide(const Fp8GemmArgs &g, int pairs, cudaStream_t st) {
 // The kernel and tile with the least estimated time: a start, and per wave of CTAs (or pairs) an end and a cost for
 // each K block, in us at 1965 MHz. Fitted to timings of each form at 1 to 64 K blocks (bf16 output, CUDA-graph
 // replay). Over 30 shapes of 1 to 22624 rows the pick was 2 % behind the fastest form on average, 11 % at
-// most; for example (us: narrow 64, narrow 128, wide 128, wide 192, wide 256)
+// most. Tiles of 16 and 32 split even where two CTAs then share an SM, if the shares are long: 8 x 10240 x 5120 takes
+// 12.3 us in 160 CTAs of 20 K blocks, 15.6 in 80 of 40; 16 x 12352 x 2048 7.4 us in 194 of 8, 7.2 in 97 of 16.
+// For example (us: narrow 64, narrow 128, wide 128, wide 192, wide 256)
 //     256 x 2048 x 4096   10.3, 13.4, 14.1, 16.6, 19.0      1024 x 2048 x 4096   27.1, 18.7, 15.2, 17.8, 20.0
 //     128 x 2048 x 4096    8.5, 10.8, 13.9, 16.6, 19.2      4096 x 1024 x 2048   30.7, 20.9, 15.9, 19.0, 13.6
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st) {
@@ -885,19 +887,23 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st) {
     int form = 0, split = 1;
     const int64_t nt = (g.N + 127) / 128;
     for (int i = 0; i < 4; ++i) {
-        const int64_t ctas = nt * ((g.M + narrow[i].tile - 1) / narrow[i].tile);
-        // K split as far as there is an SM for every CTA, all clusters run at once and every CTA keeps two K blocks
-        int lg = 0;
-        while (lg < 3 && ctas * (2 << lg) <= dev.sms && ctas <= (int64_t)(narrow[i].tile <= 32 ? 2 : 1) * dev.clusters[lg + 1] &&
-               kb >= 4 << lg)
-            ++lg;
-        const int64_t waves = ((ctas << lg) + dev.sms - 1) / dev.sms;
-        const float t = narrow[i].start + (float)waves * (narrow[i].end + (float)((kb + (1 << lg) - 1) >> lg) * narrow[i].block) +
-                        (lg ? narrow[i].push : 0.0f);
-        if (t < best) {
-            best = t;
-            form = i;
-            split = 1 << lg;
+        const int64_t mt = (g.M + narrow[i].tile - 1) / narrow[i].tile, ctas = nt * mt;
+        if (mt > 65535) continue;   // grid y
+        // K split while all clusters run at once and every CTA keeps two K blocks
+        const int per_sm = narrow[i].tile <= 32 ? 2 : 1;
+        for (int lg = 0; lg < 4; ++lg) {
+            if (lg && (ctas << lg > (int64_t)per_sm * dev.sms || ctas > (int64_t)per_sm * dev.clusters[lg] || kb < 2 << lg)) break;
+            // of two CTAs on one SM a K block each takes 1.6 times as long as one alone, and they start later
+            const bool two = per_sm == 2 && ctas << lg > dev.sms;
+            const int64_t at_once = two ? 2 * dev.sms : dev.sms, waves = ((ctas << lg) + at_once - 1) / at_once;
+            const float block = two ? 1.6f * narrow[i].block : narrow[i].block;
+            const float t = narrow[i].start + (float)waves * (narrow[i].end + (float)((kb + (1 << lg) - 1) >> lg) * block) +
+                            (lg ? narrow[i].push : 0.0f) + (two ? 1.0f : 0.0f);
+            if (t < best) {
+                best = t;
+                form = i;
+                split = 1 << lg;
+            }
         }
         if (narrow[i].tile >= g.M) break;   // wider tiles hold nothing more
     }

@@ -295,7 +295,7 @@ GDN_API gdn_status q4k_gemm(const void *a, const uint8_t *w, int32_t M, int32_t 
  * fp8_quantize_act: blocks of 1 x 128; xq [M, K] E4M3 codes, xs [M, ceil(K / 128)] fp32.
  * fp8_quantize_weight: blocks of 128 x 128; wq [N, K], ws [ceil(N / 128), ceil(K / 128)].
  * A last block past the edge of the matrix holds what is left. Supported: K % 16 == 0, M, N >= 0,
- * M * ceil(K / 128) < 2^31. */
+ * M * ceil(K / 128) < 2^31 (N in place of M for the weight), M, N, K <= 2^31 - 256. */
 GDN_API gdn_status fp8_quantize_act(const void *x, int64_t ldx, gdn_dtype in_dtype, int32_t M, int32_t K,
                                     uint8_t *xq, float *xs, gdn_stream_t stream);
 GDN_API gdn_status fp8_quantize_weight(const void *w, int64_t ldw, gdn_dtype in_dtype, int32_t N, int32_t K,
@@ -315,7 +315,9 @@ GDN_API gdn_status gdn_gated_rmsnorm_silu_fp8(const void *o, const void *z, cons
  * aq [M, K], as [M, ceil(K / 128)]: activations as fp8_quantize_act writes them; bq [N, K] (K contiguous),
  * bs [ceil(N / 128), ceil(K / 128)]: a weight as fp8_quantize_weight writes it; y [M, N] in `out_dtype`.
  * Modules stacked along N need no factors of their own where each starts at a multiple of 128.
- * Supported: K % 16 == 0, N % 16 == 0, M >= 0, M <= 128 * 65535. */
+ * as * bs is formed first, in fp32: where that product leaves fp32's range, so does y. The order of the
+ * sums depends on M, N and K alone; a call repeats bit for bit.
+ * Supported: K % 16 == 0, K >= 16, N % 16 == 0, M >= 0, M <= 128 * 65535, N, K <= 2^31 - 256. */
 GDN_API gdn_status fp8_gemm(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs, int32_t M,
                             int32_t N, int32_t K, gdn_dtype out_dtype, void *y, gdn_stream_t stream);
 

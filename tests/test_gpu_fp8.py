@@ -169,7 +169,10 @@ def check_gemm(y, aq, as_, bq, bs):
 @pytest.mark.parametrize("M,N,K", [(1, 16, 16), (1, 2048, 4096), (3, 144, 144), (16, 272, 2064), (17, 128, 128), (32, 2048, 512),
                                    (33, 16, 8192), (64, 1040, 1040), (65, 128, 256), (128, 12352, 2048), (129, 48, 400),
                                    (256, 4096, 128), (300, 1040, 2064), (511, 528, 5120), (1024, 2048, 640), (2100, 784, 1552),
-                                   (4096, 1024, 2048), (5000, 2064, 272)])
+                                   (4096, 1024, 2048), (5000, 2064, 272),
+                                   # K split over two, four and eight CTAs at each tile width, uneven shares among them
+                                   (5, 4096, 2064), (16, 6208, 8192), (8, 10240, 5136), (30, 2048, 4112), (64, 1024, 2320),
+                                   (100, 1024, 4112), (128, 4096, 8208), (200, 1024, 8192), (75, 5280, 6048)])
 @pytest.mark.parametrize("out", [BF, F32])
 def test_gemm(g, M, N, K, out):
     ops = gemm_operands(M, N, K, M + N + K)
@@ -212,6 +215,32 @@ def test_gemm_large_output_offsets(g):
     assert y.numel() > 2 ** 31
     for sl in (slice(0, 200), slice(M - 200, M)):
         check_gemm(y[sl], aq[sl], as_[sl], bq, bs)
+
+
+def test_gemm_many_rows(g):
+    """More row tiles of 16 than a grid has rows."""
+    ops = gemm_operands(1100000, 16, 16, 3)
+    check_gemm(g.fp8_gemm(*ops, out_dtype=F32), *ops)
+
+
+def test_two_graphs_at_once(g):
+    """Two captured chains replayed side by side on two streams, nothing of one in the other's results."""
+    chains, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i, M in enumerate((9, 300)):
+        x, ops = torch.randn(M, 2064, device="cuda").to(BF), gemm_operands(8, 1040, 2064, i)
+        want = g.fp8_gemm(*g.fp8_quantize_act(x), *ops[2:])
+        streams[i].wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=streams[i]):
+            y = g.fp8_gemm(*g.fp8_quantize_act(x), *ops[2:])
+        chains.append((graph, y, want, x, ops))
+    for _ in range(30):
+        for c, s in zip(chains, streams):
+            with torch.cuda.stream(s):
+                c[0].replay()
+    torch.cuda.synchronize()
+    for _, y, want, _, _ in chains:
+        assert torch.equal(y, want)
 
 
 def test_graph_and_streams(g):

@@ -225,6 +225,24 @@ def test_conv_planes(g):
     assert torch.equal(torch.cat(parts, 1), whole) and (whole[2] == 0).all()
 
 
+def test_two_batches_of_one_pool_at_once(g):
+    """Two calls on two streams, their slots interleaved in one pool, equal the calls made one after the other."""
+    gen = torch.Generator("cuda").manual_seed(5)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    B, Hk, Hv, slots = 40, 4, 8, 80
+    at = [torch.arange(i, slots, 2, dtype=torch.int32, device="cuda") for i in (0, 1)]
+    rows = [[r(B, Hk, 128).to(BF), r(B, Hk, 128).to(BF), r(B, Hv, 128).to(BF), r(B, Hv), r(B, Hv)] for _ in at]
+    A_log, dt_bias, pool = torch.rand(Hv, device="cuda"), torch.zeros(Hv, device="cuda"), r(slots, Hv, 128, 128)
+    one = pool.clone()
+    want = [g.gdn_decode_step_pooled(*x, A_log, dt_bias, one, s) for x, s in zip(rows, at)]
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    for x, s, o, st in zip(rows, at, outs, streams):
+        g.gdn_decode_step_pooled(*x, A_log, dt_bias, pool, s, o=o, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(pool, one) and all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
 class Layer:
     """One layer served in FP8: encode, fused input projection, convolution, delta rule + tail, output projection."""
 
