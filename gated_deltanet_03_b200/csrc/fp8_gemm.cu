@@ -154,6 +154,23 @@ __device__ __forceinline__ bool f8_warp_wait(uint64_t *bar, uint32_t parity, int
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
+// ... on two barriers, the first look at both in one instruction (even lanes at one, odd lanes at the other).
+__device__ __forceinline__ bool f8_warp_wait2(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, int *status) {
+    const bool odd = threadIdx.x & 1;
+    if (__all_sync(0xffffffffu, mbar_try_wait(odd ? b1 : b0, odd ? p1 : p0))) return true;
+    return f8_warp_wait(b0, p0, status) && f8_warp_wait(b1, p1, status);
+}
+// A look at two barriers, which the warp has to agree on.
+__device__ __forceinline__ bool f8_look2(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1) {
+    const bool odd = threadIdx.x & 1;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(odd ? b1 : b0)), "r"(odd ? p1 : p0)
+        : "memory");
+    return ok;
+}
 
 // Four consecutive values of a row of y.
 template <bool OUT_BF16>
@@ -294,8 +311,7 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         for (int s = 0, ph = 0; i < nkb; ++i) {
             const int b = i & 1;
             // the first use of each accumulator waits for nothing (the phase before the first)
-            if (!f8_warp_wait(&acc_empty[b], (uint32_t)(((i >> 1) & 1) ^ 1), status)) break;
-            if (!f8_warp_wait(&full[s], (uint32_t)ph, status)) break;
+            if (!f8_warp_wait2(&acc_empty[b], (uint32_t)(((i >> 1) & 1) ^ 1), &full[s], (uint32_t)ph, status)) break;
             tc_fence_after();
             const uint64_t off = (uint64_t)(s * (Cfg::STAGE_BYTES >> 4));
             if (f8_elect()) {
@@ -549,18 +565,13 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             const uint64_t a_desc = smem_desc(smem_u32(tile_a(0)), 16, 1024, 2), b_desc = smem_desc(smem_u32(tile_b(0)), 16, 1024, 2);
             int s = 0, b = 0;
             uint32_t ph = 0, bph = 1;   // the first use of each accumulator waits for nothing
+            bool ready = false;
             for (int it = 0; it < total; ++it) {
-                if (!f8_warp_wait(&full[s], ph, status) || !f8_warp_wait(&acc_empty[b], bph, status)) break;
+                if ((BUFS != 4 || !__all_sync(0xffffffffu, ready)) &&
+                    (!f8_warp_wait(&full[s], ph, status) || !f8_warp_wait(&acc_empty[b], bph, status)))
+                    break;
                 tc_fence_after();
-                if (f8_elect()) {
-                    const uint64_t off = (uint64_t)(s * (Cfg::STAGE_BYTES >> 4));
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        f8_mma_pair(tmem + b * BN, a_desc + off + 2 * kk, b_desc + off + 2 * kk, idesc, kk ? 1u : 0u);
-                    f8_commit_pair(&acc_full[b]);
-                    f8_commit_pair(&empty[s]);
-                }
-                __syncwarp();
+                const int s_now = s, b_now = b;
                 if (++s == STAGES) {
                     s = 0;
                     ph ^= 1;
@@ -569,6 +580,18 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                     b = 0;
                     bph ^= 1;
                 }
+                // With four accumulators the next block's barriers have most often completed: they are looked at while
+                // this block's MMAs are issued (512 x 4096 x 4096 14.4 -> 13.5 us; with two accumulators 3 to 5 % slower).
+                if constexpr (BUFS == 4) ready = f8_look2(&full[s], ph, &acc_empty[b], bph);
+                if (f8_elect()) {
+                    const uint64_t off = (uint64_t)(s_now * (Cfg::STAGE_BYTES >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        f8_mma_pair(tmem + b_now * BN, a_desc + off + 2 * kk, b_desc + off + 2 * kk, idesc, kk ? 1u : 0u);
+                    f8_commit_pair(&acc_full[b_now]);
+                    f8_commit_pair(&empty[s_now]);
+                }
+                __syncwarp();
             }
             // before the pair may free tensor memory: every MMA issued has completed (bounded)
             if (f8_elect()) f8_commit_pair(drain);
