@@ -273,6 +273,7 @@ short_conv_state_kernel(const void *__restrict__ x, int64_t ldx, const int32_t *
 // POOLED: sequence b's state is slot slots[b] of a pool. A row with a negative slot is passed over (its y stays
 // as it is), and so is one whose slot is not below num_slots or is named by an earlier row, with
 // GDN_ERR_INVALID_ARG in the status word; the look through the earlier rows runs beside the state loads.
+// 256 rows (250 live) x 8192 channels, K = 4: 6.4 us, 79 % of the measured copy rate (one wave of blocks).
 template <int K, bool POOLED>
 __global__ void __launch_bounds__(kConvThreads)
 short_conv_decode_kernel(const void *__restrict__ x, int64_t ldx, const float *__restrict__ w, int32_t B,

@@ -11,7 +11,7 @@
 // leave SMs idle; the partial sums are written into the shared memory of the CTA that stores them, which adds them in
 // rank order, so results do not depend on scheduling. They have a place of their own there, so that nothing waits for
 // another CTA's loads and MMAs (over the idle stage ring, behind a cluster barrier, the exchange took half of the 5.0 us
-// of 1 x 2048 x 4096, which now takes 4.1 to 4.4). One K block takes an SM 510 cycles at MT = 16 (waits, four MMAs and
+// of 1 x 2048 x 4096, which now takes 4.1 to 4.4). One K block takes an SM 450 cycles at MT = 16 (waits, four MMAs and
 // their commits one after another in one warp) to 870 at MT = 128.
 //   warp 0     TMA producer: weight tile (128 rows x 128 B) and activation tile (MT x 128 B) per K block;
 //   warp 1     tensor memory and the MMA issue;
@@ -32,7 +32,9 @@
 //              register split by setmaxnreg is 128 x 64 + 512 x 104 = 640 x 96, the launch's own total).
 // A K block of a 256-wide tile takes 840 cycles: the MMAs alone 512, with their signals and loads 620, and the read-back,
 // which shares tensor memory with them, the rest (reading 128 x 256 sums flat out slows a group of MMAs by 28 %).
-// 32768 x 2048 x 4096: 257 us in a burst (2.14 PFLOP/s), 290 to 300 us back to back, where the 1 kW limit holds the SMs at
+// One of a 128-wide tile takes 535, the MMAs alone 256: its 24 KB of loads come at 46 bytes a cycle (a TMA load path
+// measured at about 50), and the signals between the warps alone take 350.
+// 32768 x 2048 x 4096: 257 us in a burst (2.14 PFLOP/s), 290 to 301 us back to back, where the 1 kW limit holds the SMs at
 // 1.5 GHz.
 //
 // Every barrier wait is bounded (gdn_debug_set_wait); an expired one records GDN_ERR_TIMEOUT, issued copies
