@@ -80,6 +80,7 @@ struct NarrowCfg {
     static_assert(MT * PITCH * 4 <= STAGES * STAGE_BYTES, "the tile fits over the stage ring");
     static_assert(PART_BYTES >= part_bytes(2) && PART_BYTES >= part_bytes(4) && PART_BYTES >= part_bytes(8), "every split's shares fit");
     static_assert(STAGE_BYTES % 1024 == 0, "stage bases stay 1024-byte aligned");
+    static_assert(2 * STAGES + 10 <= 32, "a lane a barrier");
     static_assert(MT % kMaxSplit == 0, "whole columns for every CTA of a cluster");
     static_assert(SMEM <= 232448 && CTAS * (SMEM + 1024) <= 233472 && 8 * (2 * STAGES + 10) + 4 <= 512, "layout");
 };
@@ -256,22 +257,13 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     const int kb0 = (int)((int64_t)crank * kb_all >> split_log);
     const int nkb = (int)((int64_t)(crank + 1) * kb_all >> split_log) - kb0;
 
-    if (tid == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], Cfg::EPI_WARPS);
-            mbar_init(&scl_full[b], 2);
-            mbar_init(&scl_empty[b], Cfg::EPI_WARPS);
-        }
-        mbar_init(drain, 1);
-        mbar_init(parts, 1);
+    if (warp == 0) {
+        // a lane a barrier; arrivals: the promotion warps at acc_empty and scl_empty, two factor warps at scl_full, else one
+        const int b = lane - 2 * STAGES;
+        if (b < 10) mbar_init(&bars[lane], b == 2 || b == 3 || b == 6 || b == 7 ? Cfg::EPI_WARPS : b == 4 || b == 5 ? 2 : 1);
         fence_barrier_init();
         // the sums of this CTA's MT / split columns from every CTA of the cluster
-        if (Cfg::ASYNC && split > 1) mbar_arrive_expect_tx(parts, MT * 128 * 4);
+        if (Cfg::ASYNC && split > 1 && b == 9) mbar_arrive_expect_tx(parts, MT * 128 * 4);
     }
     __syncwarp();
     if (split > 1) f8_cluster_arrive();   // (below: nothing is sent to a CTA before it has come this far)
@@ -451,6 +443,7 @@ struct WideCfg {
     static constexpr int SMEM = OFF_BAR + 256 + 1024;
     static constexpr bool SPLIT_REGS = BN == 256;
     static constexpr int CH = BN == 256 ? 16 : 32;                // columns of a tensor-memory load
+    static_assert(2 * STAGES + 2 * BUFS + 1 <= 32, "a lane a barrier");
     static_assert(STAGE_BYTES % 1024 == 0 && SMEM <= 232448 && BUFS * BN <= 512 && OFF_FAC % 16 == 0, "layout");
 };
 
@@ -502,19 +495,19 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     const int num_tiles = tiles_n * ((M + 255) / 256);
     const int total = (num_tiles - pair + npairs - 1) / npairs * num_k;   // K blocks of this pair's tiles
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], rank == 0 ? 2 : 1);   // this CTA's TMA; in the leader also the peer's word that its own landed
-            mbar_init(&empty[s], 1);                  // the leader's commit
-        }
-        for (int b = 0; b < BUFS; ++b) {
-            mbar_init(&acc_full[b], 2);                 // the leader's commit, and warp 3: the K block's factors
-            mbar_init(&acc_empty[b], 2 * Cfg::WARPS);   // leader only: every promotion warp of the pair
-        }
-        mbar_init(drain, 1);
+    if (warp == 0) {
+        // A lane a barrier. Arrivals: at full[] this CTA's TMA, in the leader also the peer's word that its own landed; at
+        // empty[] and drain the leader's commit; at acc_full[] that and warp 3 (the K block's factors); at acc_empty[]
+        // (leader only) every promotion warp of the pair.
+        const int b = lane - 2 * STAGES;
+        if (b <= 2 * BUFS)
+            mbar_init(&bars[lane], lane < STAGES ? (rank == 0 ? 2 : 1) : b < 0 || b == 2 * BUFS ? 1 : b < BUFS ? 2 : 2 * Cfg::WARPS);
         fence_barrier_init();
-        tma_prefetch_desc(&map_a);
-        tma_prefetch_desc(&map_b);
+        if (lane == 0) {
+            tma_prefetch_desc(&map_a);
+            tma_prefetch_desc(&map_b);
+        }
+        __syncwarp();
     }
     // The producer's place: tile pt, K block pk of it, stage ps. Its first loads go out before the CTAs of the pair meet
     // (they touch this CTA's barriers alone).
@@ -545,7 +538,10 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
-    f8_cluster_sync();   // both CTAs' barriers are initialised and tensor memory is allocated
+    __syncthreads();
+    // Both CTAs' barriers are initialised (the fence above releases them to the cluster) and tensor memory is allocated.
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    f8_cluster_wait();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
