@@ -374,7 +374,7 @@ static gdn_status pooled_decode(gdn::PooledDecodeArgs &d, int32_t Dk, int32_t Dv
         return GDN_ERR_INVALID_ARG;
     if (!dtype_ok(gate_dtype) || !dtype_ok(in_dtype) || !dtype_ok(out_dtype)) return GDN_ERR_INVALID_ARG;
     if (Dk != 128 || Dv != 128 || in_dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
-    if ((int64_t)d.B * d.Hv > INT32_MAX) return GDN_ERR_UNSUPPORTED;
+    if (d.B > 65535 || (int64_t)d.B * d.Hv > INT32_MAX) return GDN_ERR_UNSUPPORTED;
     if (d.B == 0) return GDN_OK;
     if (!d.q || !d.k || !d.v || !d.a || !d.b || !d.A_log || !d.dt_bias || !d.slots || (!d.pool && d.num_slots > 0))
         return GDN_ERR_INVALID_ARG;

@@ -284,6 +284,15 @@ GDN_DEV bool mbar_wait(uint64_t *bar, uint32_t parity, int *status) {
     }
 }
 
+// True in one lane of a whole warp. A warp that issues copies or MMAs runs its loop with all lanes and elects one
+// around the instructions alone: their operands are warp-uniform registers, and from inside a one-lane branch each
+// MMA took about 90 cycles to issue, more than it ran.
+GDN_DEV bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // 2-D TMA tile load into shared memory, completing on `bar` (transaction bytes).
 GDN_DEV void tma_load_2d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int32_t x, int32_t y) {
     asm volatile(

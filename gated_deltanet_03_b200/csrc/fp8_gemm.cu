@@ -143,14 +143,6 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[N]) {
 __device__ __forceinline__ void f8_tmem_ld(uint32_t at, uint32_t (&d)[16]) { tmem_ld16(at, d); }
 __device__ __forceinline__ void f8_tmem_ld(uint32_t at, uint32_t (&d)[32]) { tmem_ld32(at, d); }
 
-// One lane of a whole warp. The warps that issue copies and MMAs run their loops with all lanes, the wait
-// included, and elect a lane around the instructions alone: the operands of those instructions are warp-uniform
-// registers, and from inside a one-lane branch each MMA took about 90 cycles to issue, more than it ran.
-__device__ __forceinline__ bool f8_elect() {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-    return ok != 0;
-}
 // The whole warp waits (bounded); false in every lane if any lane's wait ran out. The first look is apart from
 // the bounded loop: with it a wait for a phase that is over takes 60 cycles, through the loop's code 120.
 __device__ __forceinline__ bool f8_warp_wait(uint64_t *bar, uint32_t parity, int *status) {
@@ -283,7 +275,7 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         int i = 0;
         for (int s = 0, ph = 1; i < nkb; ++i) {
             if (!f8_warp_wait(&empty[s], (uint32_t)ph, status)) break;
-            if (f8_elect()) {
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
                 tma_load_2d(tile_w(s), &map_w, &full[s], (kb0 + i) * 128, n0);
                 tma_load_2d(tile_x(s), &map_x, &full[s], (kb0 + i) * 128, m0);
@@ -308,7 +300,7 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             if (!f8_warp_wait2(&acc_empty[b], (uint32_t)(((i >> 1) & 1) ^ 1), &full[s], (uint32_t)ph, status)) break;
             tc_fence_after();
             const uint64_t off = (uint64_t)(s * (Cfg::STAGE_BYTES >> 4));
-            if (f8_elect()) {
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     f8_mma(tmem + b * MT, w_desc + off + 2 * kk, x_desc + off + 2 * kk, idesc, kk ? 1u : 0u);
@@ -323,7 +315,7 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         }
         // before tensor memory is freed: every MMA issued has completed (bounded)
         if (i) {
-            if (f8_elect()) tc_commit(drain);
+            if (elect_one()) tc_commit(drain);
             __syncwarp();
             mbar_wait(drain, 0, status);
         }
@@ -513,7 +505,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     // (they touch this CTA's barriers alone).
     int pt = pair, pk = 0, pit = 0, ps = 0, pm = pair / tiles_n * 256 + rank * 128, pn = pair % tiles_n * BN + rank * (BN / 2);
     auto load_stage = [&] {
-        if (f8_elect()) {
+        if (elect_one()) {
             mbar_arrive_expect_tx(&full[ps], Cfg::STAGE_BYTES);
             tma_load_2d(tile_a(ps), &map_a, &full[ps], pk * 128, pm);
             tma_load_2d(tile_b(ps), &map_b, &full[ps], pk * 128, pn);
@@ -581,7 +573,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 // With four accumulators the next block's barriers have most often completed: they are looked at while
                 // this block's MMAs are issued (512 x 4096 x 4096 14.4 -> 13.5 us; with two accumulators 3 to 5 % slower).
                 if constexpr (BUFS == 4) ready = f8_look2(&full[s], ph, &acc_empty[b], bph);
-                if (f8_elect()) {
+                if (elect_one()) {
                     const uint64_t off = (uint64_t)(s_now * (Cfg::STAGE_BYTES >> 4));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
@@ -592,7 +584,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 __syncwarp();
             }
             // before the pair may free tensor memory: every MMA issued has completed (bounded)
-            if (f8_elect()) f8_commit_pair(drain);
+            if (elect_one()) f8_commit_pair(drain);
             __syncwarp();
             mbar_wait(drain, 0, status);
         } else if (warp == 2 && lane == 0 && rank == 1) {

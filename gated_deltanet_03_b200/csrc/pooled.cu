@@ -7,12 +7,12 @@
 // HBM-bound: 128 KB of state traffic and about 8 operations a state value per (row, head) item. The grid has one
 // CTA per unit of one or more heads of a row; those that run take over the units of CTAs that have not been
 // launched yet (cluster launch control), so each SM does as many as its share of the memory rate allows (equal
-// shares left the fastest SMs idle for a fifth of the time: 188 us against 169 for 256 rows x 32 heads). A
+// shares left the fastest SMs idle for a fifth of the time: 188 us against 166 for 256 rows x 32 heads). A
 // producer warp brings each item's 64 KB state and its q, k, v, z rows into a ring by bulk copies, so loads
 // stay in flight while items are computed, written back and encoded:
 //   warps 0-15   the state from the stage into registers (8 lanes a row, 2 rows a thread, in the arithmetic of
 //                gdn_recurrent128_kernel, so o and S equal gdn_decode_step's bit for bit), the stage released
-//                at once, the update, S stored straight to the pool, o to shared memory;
+//                at once, the update, o to shared memory, S stored straight to the pool;
 //   warp 16      slots, bulk copies, gates;
 //   warps 17-18  item i's o row on warp 17 + i % 2 (tail and encode, or the plain store). Its chain of
 //                reductions and divisions takes longer than the update; done in turn by the update's own warps
@@ -69,21 +69,23 @@ __device__ __forceinline__ void claim_unit(uint4 *answer, uint64_t *bar) {
                  "r"(smem_u32(bar))
                  : "memory");
 }
-// The claimed unit (that CTA's index), or -1 if none was left.
-__device__ __forceinline__ int claimed_unit(const uint4 *answer) {
-    uint32_t ok, x;
+// The claimed unit (grid y and x of that CTA: row and place in it), or row -1 if none was left.
+__device__ __forceinline__ int2 claimed_unit(const uint4 *answer) {
+    uint32_t ok, x, y;
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
-        "ld.shared.b128 r, [%2];\n\t"
+        "ld.shared.b128 r, [%3];\n\t"
         "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t"
         "mov.u32 %1, 0;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
-        : "=r"(ok), "=r"(x)
+        "mov.u32 %2, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::y.b32.b128 %2, r;\n\t}"
+        : "=r"(ok), "=r"(x), "=r"(y)
         : "r"(smem_u32(answer))
         : "memory");
     fence_proxy_async_smem();   // read before the next answer is written
-    return ok ? (int)x : -1;
+    return make_int2(ok ? (int)y : -1, (int)x);
 }
 
 __device__ __forceinline__ float pool_dot16(const f2_t (&a)[8], const f2_t (&b)[8]) {
@@ -129,16 +131,11 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
     extern __shared__ uint8_t smem_raw[];
     PoolSmem &sm = *reinterpret_cast<PoolSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    if (tid == 0) {
-        for (int s = 0; s < kPoolStages; ++s) {
-            mbar_init(&sm.full[s], 2);   // the copies, and the item's meta data
-            mbar_init(&sm.empty[s], kPoolWarps + 1);
-        }
-        for (int b = 0; b < kPoolRows; ++b) {
-            mbar_init(&sm.o_full[b], kPoolWarps);
-            mbar_init(&sm.o_empty[b], 1);
-        }
-        mbar_init(&sm.claimed, 1);
+    if (warp == 0) {
+        // a lane a barrier; full: the copies, and the item's meta data
+        constexpr int F = kPoolStages, E = 2 * F, O = E + kPoolRows, C = O + kPoolRows;
+        if (lane <= C)
+            mbar_init(&sm.full[0] + lane, lane < F ? 2 : lane < E ? kPoolWarps + 1 : lane < O ? kPoolWarps : 1);
         fence_barrier_init();
     }
     __syncthreads();
@@ -147,26 +144,35 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
     asm volatile("" : "+r"(first));    // (not known to the compiler, which would give that pass code of its own)
 
     if (warp == kPoolWarps) {
+        const int group = Hv / d.Hk;
         pdl_wait();
-        const int group = Hv / d.Hk, units_row = (Hv + d.unit_heads - 1) / d.unit_heads;
         int it = 0, claims = 0;
         bool ok = true;
-        for (int unit = blockIdx.x; unit >= 0 && ok;) {
-            if (lane == 0) claim_unit(&sm.claim, &sm.claimed);   // the next one
-            ++claims;
-            const int row = unit / units_row, h0 = (unit - row * units_row) * d.unit_heads;
+        // A unit is a row (grid y) and unit_heads heads of it (grid x: heads of a row, which lie side by side in the pool, go
+        // to CTAs that run together; the rows in front took 167 us for 256 x 32 heads, 165.7 so). From a CTA's start to its
+        // first load is time that a small batch pays in full, so the loads of the slots go out first, and the claim, the
+        // head's place and the barriers of an empty ring hold up nothing (48 items 5.6 -> 5.2 us, with the outputs in front
+        // of the stores).
+        for (int2 unit = make_int2(blockIdx.y, blockIdx.x); unit.x >= 0 && ok;) {
+            const int row = unit.x, h0 = unit.y * d.unit_heads, h1 = min(h0 + d.unit_heads, Hv);
             const int slot = d.slots[row];
-            bool again = false;
-            for (int i = lane; i < row; i += 32) again |= d.slots[i] == slot;   // an earlier row's slot
+            const int other = lane < row ? d.slots[lane] : -1;
+            if (elect_one()) claim_unit(&sm.claim, &sm.claimed);   // the next one
+            ++claims;
+            int kh = h0 / group, kr = h0 - kh * group;             // key head, and heads of it passed
+            bool again = lane < row && other == slot;              // an earlier row's slot
+            for (int i = lane + 32; i < row; i += 32) again |= d.slots[i] == slot;
             again = __any_sync(kAll, again);
             const bool live = slot >= 0 && slot < d.num_slots && !again;
             if (slot >= 0 && !live && lane == 0) report_status(d.status, GDN_ERR_INVALID_ARG);
-            for (int h = h0; live && h < min(h0 + d.unit_heads, Hv); ++h, ++it) {
+            for (int h = h0; live && h < h1; ++h, ++it) {
                 const int s = it % kPoolStages;
-                ok = warp_wait(&sm.empty[s], (uint32_t)(((it / kPoolStages) & 1) ^ 1), lane, d.status);
+                const float ga = gate_at(d.a, d.gate_bf16, row * d.ldg + h), gb = gate_at(d.b, d.gate_bf16, row * d.ldg + h);
+                const float ge = d.A_log[h], gt = d.dt_bias[h];
+                if (it >= kPoolStages) ok = warp_wait(&sm.empty[s], (uint32_t)(((it / kPoolStages) & 1) ^ 1), lane, d.status);
                 if (!ok) break;
-                if (lane == 0) {
-                    const int64_t vrow = ((int64_t)row * Hv + h) * kD, krow = ((int64_t)row * d.Hk + h / group) * kD;
+                const int64_t vrow = ((int64_t)row * Hv + h) * kD, krow = ((int64_t)row * d.Hk + kh) * kD;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&sm.full[s], kStateBytes + (TAIL ? 4 : 3) * kRowBytes);
                     bulk_load(sm.state[s], d.pool + ((int64_t)slot * Hv + h) * kD * kD, kStateBytes, &sm.full[s]);
                     bulk_load(sm.k[s], reinterpret_cast<const __nv_bfloat16 *>(d.k) + krow, kRowBytes, &sm.full[s]);
@@ -174,9 +180,15 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
                     bulk_load(sm.v[s], reinterpret_cast<const __nv_bfloat16 *>(d.v) + vrow, kRowBytes, &sm.full[s]);
                     if constexpr (TAIL)
                         bulk_load(sm.z[s], reinterpret_cast<const __nv_bfloat16 *>(d.z) + row * d.ldz + h * kD, kRowBytes, &sm.full[s]);
-                    float g, beta;   // while the state is on its way
-                    gdn_gates(gate_at(d.a, d.gate_bf16, row * d.ldg + h), gate_at(d.b, d.gate_bf16, row * d.ldg + h), d.A_log[h],
-                              d.dt_bias[h], g, beta);
+                }
+                __syncwarp();
+                if (++kr == group) {
+                    kr = 0;
+                    ++kh;
+                }
+                float g, beta;   // while the state is on its way
+                gdn_gates(ga, gb, ge, gt, g, beta);
+                if (lane == 0) {
                     sm.meta[s] = {row, h, slot, expf(g), beta};
                     mbar_arrive(&sm.full[s]);
                 }
@@ -301,6 +313,14 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
 #pragma unroll
             for (int c = 0; c < 8; ++c) st[p][c] = fma2(a2, st[p][c], mul2(u2, k2[c]));
         }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) part[p] = pool_dot16(st[p], q2);
+        const float ot = pool_sum2(part, l8) * qn;
+        // the row that this buffer held has been finished
+        if (run && !warp_wait(&sm.o_empty[ob], (uint32_t)(((it / kPoolRows) & 1) ^ 1), lane, d.status)) break;
+        if (run && (l8 & 3) == 0) sm.o[ob][rbase + 64 * (l8 >> 2)] = ot;
+        __syncwarp();
+        if (run && lane == 0) mbar_arrive(&sm.o_full[ob]);
         if (run) {
             float *out = d.pool + ((int64_t)m.slot * Hv + m.head) * kD * kD + rbase * kD + 4 * l8;
 #pragma unroll
@@ -310,14 +330,6 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
                     __stcs(reinterpret_cast<float4 *>(out + 64 * p * kD + 32 * j),
                            make_float4(f2lo(st[p][2 * j]), f2hi(st[p][2 * j]), f2lo(st[p][2 * j + 1]), f2hi(st[p][2 * j + 1])));
         }
-#pragma unroll
-        for (int p = 0; p < 2; ++p) part[p] = pool_dot16(st[p], q2);
-        const float ot = pool_sum2(part, l8) * qn;
-        // the row that this buffer held has been finished
-        if (run && !warp_wait(&sm.o_empty[ob], (uint32_t)(((it / kPoolRows) & 1) ^ 1), lane, d.status)) break;
-        if (run && (l8 & 3) == 0) sm.o[ob][rbase + 64 * (l8 >> 2)] = ot;
-        __syncwarp();
-        if (run && lane == 0) mbar_arrive(&sm.o_full[ob]);
         if (!run) pdl_wait();
     }
 }
@@ -339,8 +351,8 @@ cudaError_t launch_pooled_t(PooledDecodeArgs d, cudaStream_t st) {
     d.unit_heads = 1;
     while (d.unit_heads < d.Hv && (int64_t)d.B * ((d.Hv + 2 * d.unit_heads - 1) / (2 * d.unit_heads)) >= 16 * (int64_t)sms)
         d.unit_heads *= 2;
-    const int64_t units = (int64_t)d.B * ((d.Hv + d.unit_heads - 1) / d.unit_heads);
-    return launch_pdl(gdn_decode128_pooled_kernel<TAIL>, dim3((unsigned)units), dim3(kPoolThreads), kPoolSmem, st, d);
+    const int units_row = (d.Hv + d.unit_heads - 1) / d.unit_heads;
+    return launch_pdl(gdn_decode128_pooled_kernel<TAIL>, dim3((unsigned)units_row, (unsigned)d.B), dim3(kPoolThreads), kPoolSmem, st, d);
 }
 
 }  // namespace

@@ -329,7 +329,7 @@ GDN_API gdn_status fp8_gemm(const uint8_t *aq, const float *as, const uint8_t *b
  *        device status word then reads GDN_ERR_INVALID_ARG (gdn_get_device_status).
  * a, b   gate pre-activations in `gate_dtype`, rows of ldg elements (ldg >= Hv), so they can be column
  *        blocks of a projection's output. q, k, v, o as gdn_decode_step.
- * Supported: Dk == Dv == 128, bf16 q, k, v; Hv % Hk == 0; B >= 0, B * Hv < 2^31.
+ * Supported: Dk == Dv == 128, bf16 q, k, v; Hv % Hk == 0; 0 <= B <= 65535, B * Hv < 2^31.
  * o and the states equal gdn_decode_step's on the same rows bit for bit. */
 GDN_API gdn_status gdn_decode_step_pooled(const void *q, const void *k, const void *v, const void *a, const void *b,
                                           int64_t ldg, gdn_dtype gate_dtype, const float *A_log,

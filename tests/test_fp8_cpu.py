@@ -66,7 +66,7 @@ def test_pooled_decode_refusals(fn):
     for bad in (dict(Hv=3, Hk=2), dict(ldg=3), dict(gate=3), dict(io=9), dict(slots=-1), dict(B=-1), dict(q=None), dict(q=A + 8),
                 dict(at=None), dict(pool=None), dict(pool=A + 4), dict(A_log=None), dict(a=None), dict(o=A + 2)):
         assert pooled(fn, **bad) == BAD, bad
-    for bad in (dict(Dk=64, Dv=64, ldz=4096), dict(io=FP32), dict(B=2 ** 30)):
+    for bad in (dict(Dk=64, Dv=64, ldz=4096), dict(io=FP32), dict(B=2 ** 30), dict(B=65536)):
         assert pooled(fn, **bad) == UNSUPPORTED, bad
     assert pooled(fn, B=0, q=None, at=None) == OK
 
