@@ -436,7 +436,7 @@ struct WideCfg {
     static constexpr bool SPLIT_REGS = BN == 256;
     static constexpr int CH = BN == 256 ? 16 : 32;                // columns of a tensor-memory load
     static_assert(2 * STAGES + 2 * BUFS + 1 <= 32, "a lane a barrier");
-    static_assert(STAGE_BYTES % 1024 == 0 && SMEM <= 232448 && BUFS * BN <= 512 && OFF_FAC % 16 == 0, "layout");
+    static_assert(STAGE_BYTES % 1024 == 0 && kWPieceBytes % 512 == 0 && SMEM <= 232448 && BUFS * BN <= 512 && OFF_FAC % 16 == 0, "layout");
 };
 
 // Arrival on a barrier of a CTA of the pair (no generic-memory data goes with it).
@@ -457,6 +457,14 @@ __device__ __forceinline__ void f8_mma_pair(uint32_t d, uint64_t a, uint64_t b, 
 }
 // acc += f * d on CH accumulator columns. (Scalar FMAs: as packed f32x2 ones they need the loaded columns in
 // aligned register pairs, and the moves and spills cost a fifth of the kernel's time.)
+// A tile of 64-byte rows from shared memory to the matrix of `map`, in a bulk group of its own.
+__device__ __forceinline__ void f8_store_2d(const CUtensorMap *map, const void *smem, int32_t x, int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+        "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "r"(smem_u32(smem)), "r"(x), "r"(y)
+        : "memory");
+}
 template <int CH>
 __device__ __forceinline__ void f8_promote(float *acc, const uint32_t (&d)[CH], float f) {
 #pragma unroll
@@ -466,8 +474,9 @@ __device__ __forceinline__ void f8_promote(float *acc, const uint32_t (&d)[CH], 
 template <int BN, bool OUT_BF16>
 __global__ void __launch_bounds__(WideCfg<BN>::THREADS, 1)
 fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                     const __grid_constant__ CUtensorMap map_y,
                      const float *__restrict__ as, const float *__restrict__ bs, int M, int N, int num_k,
-                     void *__restrict__ y, int *status) {
+                     int *status) {
     using Cfg = WideCfg<BN>;
     constexpr int STAGES = Cfg::STAGES, BUFS = Cfg::BUFS;
     pdl_launch_dependents();
@@ -498,6 +507,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         if (lane == 0) {
             tma_prefetch_desc(&map_a);
             tma_prefetch_desc(&map_b);
+            tma_prefetch_desc(&map_y);
         }
         __syncwarp();
     }
@@ -687,13 +697,15 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 }
             }
             if (!ok) break;
-            // a row of y lies in one thread: pieces of 32 rows x 64 bytes turn in the warp's shared memory
-            // (16-byte chunk c of row r at chunk c ^ (r / 2 % 4): no bank conflicts either way) so that a store
-            // covers eight runs of 64 bytes instead of 32 of 16
+            // A row of y lies in one thread: pieces of 32 rows x 64 bytes go through the warp's shared memory (16-byte chunk
+            // c of row r at chunk c ^ (r / 2 % 4), the 64-byte swizzle) and out by TMA, which leaves off what lies past
+            // the last row or column. Read back and stored by the warps, eight rows a store, they kept the SM's store
+            // path busy for 1,600 to 2,600 cycles a tile.
             constexpr int CPP = OUT_BF16 ? 32 : 16;      // columns per piece
             const int m_base = t / tiles_n * 256 + r0, n_base = t % tiles_n * BN + group * 64;
 #pragma unroll
             for (int pc = 0; pc < 64 / CPP; ++pc) {
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the piece before is out
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -712,17 +724,12 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                     }
                     *reinterpret_cast<uint4 *>(piece + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = u;
                 }
+                fence_proxy_async_smem();
                 __syncwarp();
-                const int c = lane & 3, n = n_base + pc * CPP + c * (CPP / 4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 8 * i + lane / 4;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(piece + r * 64 + ((c ^ (r >> 1 & 3)) << 4));
-                    if (m_base + r < M && n < N)
-                        *reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(y) + ((int64_t)(m_base + r) * N + n) * (OUT_BF16 ? 2 : 4)) = u;
-                }
+                if (lane == 0 && m_base < M && n_base + pc * CPP < N) f8_store_2d(&map_y, piece, n_base + pc * CPP, m_base);
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     // Neither CTA frees tensor memory or exits while the pair's MMAs, reads or arrivals may touch it. Relaxed: no data of
@@ -766,6 +773,19 @@ bool f8_map(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t K, uint32_t
     cuuint32_t elem[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, elem,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// y [M, N], boxes of 32 rows x 64 bytes, 64-byte swizzle.
+bool f8_map_out(CUtensorMap *m, void *ptr, uint64_t M, uint64_t N, bool bf16) {
+    EncodeTiledFn fn = f8_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {N, M};
+    cuuint64_t strides[1] = {N * (bf16 ? 2 : 4)};
+    cuuint32_t box[2] = {bf16 ? 32u : 16u, 32};
+    cuuint32_t elem[2] = {1, 1};
+    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, ptr, dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -851,8 +871,9 @@ cudaError_t launch_narrow(const Fp8GemmArgs &g, int split, cudaStream_t st) {
 template <int BN>
 cudaError_t launch_wide(const Fp8GemmArgs &g, int pairs, cudaStream_t st) {
     using Cfg = WideCfg<BN>;
-    CUtensorMap ma, mb;
-    if (!f8_map(&ma, g.aq, (uint64_t)g.M, (uint64_t)g.K, 128) || !f8_map(&mb, g.bq, (uint64_t)g.N, (uint64_t)g.K, BN / 2))
+    CUtensorMap ma, mb, my;
+    if (!f8_map(&ma, g.aq, (uint64_t)g.M, (uint64_t)g.K, 128) || !f8_map(&mb, g.bq, (uint64_t)g.N, (uint64_t)g.K, BN / 2) ||
+        !f8_map_out(&my, g.y, (uint64_t)g.M, (uint64_t)g.N, g.out_bf16))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     const int64_t tiles = (int64_t)((g.N + BN - 1) / BN) * ((g.M + 255) / 256);
@@ -870,8 +891,8 @@ cudaError_t launch_wide(const Fp8GemmArgs &g, int pairs, cudaStream_t st) {
     cfg.attrs = attrs;
     cfg.numAttrs = 2;
     const int kb = (g.K + 127) / 128;
-    if (g.out_bf16) return cudaLaunchKernelEx(&cfg, fp8_gemm_wide_kernel<BN, true>, ma, mb, g.as, g.bs, g.M, g.N, kb, g.y, g.status);
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_wide_kernel<BN, false>, ma, mb, g.as, g.bs, g.M, g.N, kb, g.y, g.status);
+    if (g.out_bf16) return cudaLaunchKernelEx(&cfg, fp8_gemm_wide_kernel<BN, true>, ma, mb, my, g.as, g.bs, g.M, g.N, kb, g.status);
+    return cudaLaunchKernelEx(&cfg, fp8_gemm_wide_kernel<BN, false>, ma, mb, my, g.as, g.bs, g.M, g.N, kb, g.status);
 }
 
 }  // namespace
