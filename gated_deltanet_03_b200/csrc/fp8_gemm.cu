@@ -427,10 +427,10 @@ struct WideCfg {
     static constexpr int BUFS = BN == 128 ? 4 : 2;                // accumulators in tensor memory
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = BN == 256 ? 5 : BN == 192 ? 6 : 8;
+    static constexpr int STAGES = BN == 256 ? 4 : BN == 192 ? 6 : 7;
     static constexpr int FAC_SLOTS = kWFacAhead + 2 * BUFS;
     static constexpr int OFF_OUT = STAGES * STAGE_BYTES;
-    static constexpr int OFF_FAC = OFF_OUT + WARPS * kWPieceBytes;
+    static constexpr int OFF_FAC = OFF_OUT + WARPS * 2 * kWPieceBytes;
     static constexpr int OFF_BAR = OFF_FAC + FAC_SLOTS * kWFacPitch * 4;
     static constexpr int SMEM = OFF_BAR + 256 + 1024;
     static constexpr bool SPLIT_REGS = BN == 256;
@@ -457,11 +457,10 @@ __device__ __forceinline__ void f8_mma_pair(uint32_t d, uint64_t a, uint64_t b, 
 }
 // acc += f * d on CH accumulator columns. (Scalar FMAs: as packed f32x2 ones they need the loaded columns in
 // aligned register pairs, and the moves and spills cost a fifth of the kernel's time.)
-// A tile of 64-byte rows from shared memory to the matrix of `map`, in a bulk group of its own.
+// A tile of 64-byte rows from shared memory to the matrix of `map`.
 __device__ __forceinline__ void f8_store_2d(const CUtensorMap *map, const void *smem, int32_t x, int32_t y) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
-        "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
         "r"(smem_u32(smem)), "r"(x), "r"(y)
         : "memory");
 }
@@ -663,7 +662,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         const uint32_t tm = tmem + ((uint32_t)(quarter * 32) << 16) + group * 64;
         const uint32_t leader_empty = f8_mapa(acc_empty, 0);
         const int r0 = rank * 128 + quarter * 32;
-        uint8_t *piece = sm + Cfg::OFF_OUT + (warp - 4) * kWPieceBytes;
+        uint8_t *pieces = sm + Cfg::OFF_OUT + (warp - 4) * 2 * kWPieceBytes;
         const float *fac = reinterpret_cast<const float *>(sm + Cfg::OFF_FAC);
         int fslot = 0, b = 0;
         uint32_t bph = 0;
@@ -705,7 +704,8 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             const int m_base = t / tiles_n * 256 + r0, n_base = t % tiles_n * BN + group * 64;
 #pragma unroll
             for (int pc = 0; pc < 64 / CPP; ++pc) {
-                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the piece before is out
+                uint8_t *piece = pieces + pc % 2 * kWPieceBytes;
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the one before last is out
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -726,7 +726,10 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0 && m_base < M && n_base + pc * CPP < N) f8_store_2d(&map_y, piece, n_base + pc * CPP, m_base);
+                if (lane == 0) {
+                    if (m_base < M && n_base + pc * CPP < N) f8_store_2d(&map_y, piece, n_base + pc * CPP, m_base);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");   // (one a piece: the waits count them)
+                }
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
