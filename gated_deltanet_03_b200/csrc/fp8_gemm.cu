@@ -34,7 +34,10 @@
 // which shares tensor memory with them, the rest (reading 128 x 256 sums flat out slows a group of MMAs by 28 %).
 // One of a 128-wide tile takes 535, the MMAs alone 256: its 24 KB of loads come at 46 bytes a cycle (a TMA load path
 // measured at about 50), and the signals between the warps alone take 350.
-// 32768 x 2048 x 4096: 257 us in a burst (2.14 PFLOP/s), 290 to 301 us back to back, where the 1 kW limit holds the SMs at
+// With the accumulators neither read back nor added a call of 8192 x 2048 x 4096 takes 58 us instead of 70, without its
+// MMAs 60, with a third of its loads 68: at 256 columns it is the way from an accumulator's MMAs through its promotion to
+// the next ones, with two accumulators in turn, that sets the pace.
+// 32768 x 2048 x 4096: 245 us in a burst (2.24 PFLOP/s), 262 to 284 us back to back, where the 1 kW limit holds the SMs at
 // 1.5 GHz.
 //
 // Every barrier wait is bounded (gdn_debug_set_wait); an expired one records GDN_ERR_TIMEOUT, issued copies
@@ -48,8 +51,8 @@ namespace {
 constexpr int kChunk = 8;                  // K blocks per set of staged factors
 constexpr int kMaxSplit = 8;
 // Stages loaded before the CTAs of a pair meet: from the producer's loop the first load left 1,600 cycles later (256 x
-// 12352 x 2048 in 11.4 us, now 11.0); but a stage takes 300 cycles to issue, and with all of them first the rest of
-// the pair waited for that.
+// 12352 x 2048 11.4 us against 11.0); but a stage takes 200 to 300 cycles to issue, and with all of them first the rest
+// of the pair waited for that.
 constexpr int kEarly = 2;
 
 template <int MT>
@@ -434,7 +437,7 @@ struct WideCfg {
     static constexpr int OFF_BAR = OFF_FAC + FAC_SLOTS * kWFacPitch * 4;
     static constexpr int SMEM = OFF_BAR + 256 + 1024;
     static constexpr bool SPLIT_REGS = BN == 256;
-    static constexpr int CH = BN == 256 ? 16 : 32;                // columns of a tensor-memory load
+    static constexpr int CH = 32;                // columns of a tensor-memory load
     static_assert(2 * STAGES + 2 * BUFS + 1 <= 32, "a lane a barrier");
     static_assert(STAGE_BYTES % 1024 == 0 && kWPieceBytes % 512 == 0 && SMEM <= 232448 && BUFS * BN <= 512 && OFF_FAC % 16 == 0, "layout");
 };
@@ -455,8 +458,6 @@ __device__ __forceinline__ void f8_mma_pair(uint32_t d, uint64_t a, uint64_t b, 
         "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
-// acc += f * d on CH accumulator columns. (Scalar FMAs: as packed f32x2 ones they need the loaded columns in
-// aligned register pairs, and the moves and spills cost a fifth of the kernel's time.)
 // A tile of 64-byte rows from shared memory to the matrix of `map`.
 __device__ __forceinline__ void f8_store_2d(const CUtensorMap *map, const void *smem, int32_t x, int32_t y) {
     asm volatile(
@@ -464,10 +465,12 @@ __device__ __forceinline__ void f8_store_2d(const CUtensorMap *map, const void *
         "r"(smem_u32(smem)), "r"(x), "r"(y)
         : "memory");
 }
+// acc += f * d on CH accumulator columns, two at a time. (The sums are kept as pairs everywhere: packed and unpacked here
+// they cost a fifth of the kernel's time in moves and spills.)
 template <int CH>
-__device__ __forceinline__ void f8_promote(float *acc, const uint32_t (&d)[CH], float f) {
+__device__ __forceinline__ void f8_promote(f2_t *acc, const uint32_t (&d)[CH], f2_t f) {
 #pragma unroll
-    for (int j = 0; j < CH; ++j) acc[j] = fmaf(__uint_as_float(d[j]), f, acc[j]);
+    for (int j = 0; j < CH; j += 2) acc[j / 2] = fma2(f2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])), f, acc[j / 2]);
 }
 
 template <int BN, bool OUT_BF16>
@@ -668,26 +671,28 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         uint32_t bph = 0;
         bool ok = true;
         for (int t = pair; t < num_tiles && ok; t += npairs) {
-            float acc[64];
+            f2_t acc[32];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) acc[j] = 0.0f;
+            for (int j = 0; j < 32; ++j) acc[j] = 0ull;
             for (int k = 0; k < num_k; ++k) {
                 if (!(ok = f8_warp_wait(&acc_full[b], bph, status))) break;
                 tc_fence_after();
-                uint32_t d[2][CH];   // CH columns are loaded while the CH before are added
-                f8_tmem_ld(tm + b * BN, d[0]);
-                const float f = fac[fslot * kWFacPitch + quarter * 32 + lane] * fac[fslot * kWFacPitch + 128 + group];
+                // two loads of 32 columns in one set of registers (four of 16 in two sets, each under way while the one
+                // before was added, with scalar sums: 32768 x 2048 x 4096 282 us back to back, so 267)
+                uint32_t d[CH];
+                f8_tmem_ld(tm + b * BN, d);
+                const float f1 = fac[fslot * kWFacPitch + quarter * 32 + lane] * fac[fslot * kWFacPitch + 128 + group];
+                const f2_t f = f2(f1, f1);
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
-                    tmem_ld_wait_for(d[c & 1]);
-                    if (c + 1 < NCH) {
-                        f8_tmem_ld(tm + b * BN + CH * (c + 1), d[(c + 1) & 1]);
-                    } else {
+                    tmem_ld_wait_for(d);
+                    if (c == NCH - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) f8_arrive_at(leader_empty + (uint32_t)(b * 8));
                     }
-                    f8_promote(acc + CH * c, d[c & 1], f);
+                    f8_promote(acc + CH / 2 * c, d, f);
+                    if (c + 1 < NCH) f8_tmem_ld(tm + b * BN + CH * (c + 1), d);
                 }
                 if (++fslot == Cfg::FAC_SLOTS) fslot = 0;
                 if (++b == BUFS) {
@@ -709,18 +714,18 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 __syncwarp();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const float *v = acc + CPP * pc + CPP / 4 * c;
+                    const f2_t *v = acc + (CPP * pc + CPP / 4 * c) / 2;
                     uint4 u;
                     if constexpr (OUT_BF16) {
                         uint32_t w[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const __nv_bfloat162 p2 = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                            const __nv_bfloat162 p2 = __floats2bfloat162_rn(f2lo(v[j]), f2hi(v[j]));
                             w[j] = *reinterpret_cast<const uint32_t *>(&p2);
                         }
                         u = make_uint4(w[0], w[1], w[2], w[3]);
                     } else {
-                        u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+                        u = make_uint4(__float_as_uint(f2lo(v[0])), __float_as_uint(f2hi(v[0])), __float_as_uint(f2lo(v[1])), __float_as_uint(f2hi(v[1])));
                     }
                     *reinterpret_cast<uint4 *>(piece + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)) = u;
                 }
@@ -902,12 +907,12 @@ cudaError_t launch_wide(const Fp8GemmArgs &g, int pairs, cudaStream_t st) {
 
 // The kernel and tile with the least estimated time: a start, and per wave of CTAs (or pairs) an end and a cost for
 // each K block, in us at 1965 MHz. Fitted to timings of each form at 1 to 64 K blocks (bf16 output, CUDA-graph
-// replay). Over 30 shapes of 1 to 22624 rows the pick was 2 % behind the fastest form on average, 11 % at
-// most. Tiles of 16 and 32 split even where two CTAs then share an SM, if the shares are long: 8 x 10240 x 5120 takes
+// replay). Over 58 shapes of 1 to 26020 rows the pick was 1 to 2 % behind the fastest form on average, 6 % at most.
+// Tiles of 16 and 32 split even where two CTAs then share an SM, if the shares are long: 8 x 10240 x 5120 takes
 // 12.3 us in 160 CTAs of 20 K blocks, 15.6 in 80 of 40; 16 x 12352 x 2048 7.4 us in 194 of 8, 7.2 in 97 of 16.
 // For example (us: narrow 64, narrow 128, wide 128, wide 192, wide 256)
-//     256 x 2048 x 4096   10.3, 13.4, 14.1, 16.6, 19.0      1024 x 2048 x 4096   27.1, 18.7, 15.2, 17.8, 20.0
-//     128 x 2048 x 4096    8.5, 10.8, 13.9, 16.6, 19.2      4096 x 1024 x 2048   30.7, 20.9, 15.9, 19.0, 13.6
+//     256 x 2048 x 4096   10.2, 13.2, 12.4, 15.7, 17.7      1024 x 2048 x 4096   26.0, 18.6, 13.5, 16.6, 18.8
+//     128 x 2048 x 4096    8.1, 10.7, 12.3, 15.4, 17.6      256 x 12352 x 2048   24.3, 21.2, 13.8, 10.9, 12.5
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st) {
     Fp8Device dev;
     const cudaError_t e = f8_device(&dev);
@@ -919,7 +924,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st) {
     };
     static const Form narrow[4] = {{16, 2.1f, 1.0f, 0.26f, 0.4f}, {32, 2.2f, 1.0f, 0.285f, 0.9f}, {64, 2.7f, 1.0f, 0.31f, 1.1f},
                                    {128, 3.6f, 1.0f, 0.42f, 2.3f}};
-    static const Form wide[3] = {{128, 3.2f, 0.8f, 0.311f, 0.0f}, {192, 3.8f, 1.0f, 0.381f, 0.0f}, {256, 4.2f, 1.2f, 0.4275f, 0.0f}};
+    static const Form wide[3] = {{128, 3.1f, 0.8f, 0.285f, 0.0f}, {192, 3.7f, 1.0f, 0.36f, 0.0f}, {256, 4.0f, 1.2f, 0.415f, 0.0f}};
     float best = 3.0e38f;
     int form = 0, split = 1;
     const int64_t nt = (g.N + 127) / 128;
