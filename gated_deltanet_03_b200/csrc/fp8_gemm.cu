@@ -94,11 +94,9 @@ __device__ __forceinline__ uint32_t f8_cluster_rank() {
     return r;
 }
 __device__ __forceinline__ void f8_cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// ... with nothing to release: an arrival that releases holds its warp up for about 1,000 cycles.
+__device__ __forceinline__ void f8_cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void f8_cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void f8_cluster_sync() {
-    f8_cluster_arrive();
-    f8_cluster_wait();
-}
 // The shared::cluster address of this CTA's object `p` in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t f8_mapa(const void *p, uint32_t rank) {
     uint32_t r;
@@ -261,7 +259,8 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         if (Cfg::ASYNC && split > 1 && b == 9) mbar_arrive_expect_tx(parts, MT * 128 * 4);
     }
     __syncwarp();
-    if (split > 1) f8_cluster_arrive();   // (below: nothing is sent to a CTA before it has come this far)
+    // (below: nothing is sent to a CTA before it has come this far; the fence above releases its barriers)
+    if (split > 1) f8_cluster_arrive_relaxed();
     if (warp == 1) {
         tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
         tmem_relinquish();
@@ -400,7 +399,8 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             else f8_send_parts<MT, 2>(sm, parts, acc, warp, lane, crank, cpr);
         }
         __syncwarp();
-        f8_cluster_arrive();
+        if constexpr (Cfg::ASYNC) f8_cluster_arrive_relaxed();   // (the sums signal for themselves)
+        else f8_cluster_arrive();
         bool here = true;   // the sums of every CTA of the cluster have arrived in this one
         if constexpr (Cfg::ASYNC) here = f8_warp_wait(parts, 0, status);
         else f8_cluster_wait();
@@ -544,7 +544,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     tc_fence_before();
     __syncthreads();
     // Both CTAs' barriers are initialised (the fence above releases them to the cluster) and tensor memory is allocated.
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    f8_cluster_arrive_relaxed();
     f8_cluster_wait();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
@@ -743,7 +743,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
     // Neither CTA frees tensor memory or exits while the pair's MMAs, reads or arrivals may touch it. Relaxed: no data of
     // the other CTA is read after it, and a release would wait for the stores of y to be performed.
     tc_fence_before();
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    f8_cluster_arrive_relaxed();
     f8_cluster_wait();
     if (warp == 1) {
         tc_fence_after();
