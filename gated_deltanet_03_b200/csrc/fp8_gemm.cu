@@ -557,18 +557,24 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 if (!f8_warp_wait(&empty[ps], (uint32_t)(((pit / STAGES) & 1) ^ 1), status)) break;
                 load_stage();
             }
-            // before the CTA may exit: the latest load armed on each stage has landed
+            // before the CTA may exit: the latest load armed on each stage has landed ..
             for (int s = 0; s < STAGES && s < pit; ++s) {
                 const int last = pit - 1 - ((pit - 1 - s) % STAGES);
                 mbar_wait(&full[s], (uint32_t)((last / STAGES) & 1), status);
             }
+            // .. and the leader's commit of the MMAs that read it has arrived here: the loop's waits, STAGES blocks on
+            for (int i = pit; pit == total && i < total + STAGES; ++i) {
+                if (!f8_warp_wait(&empty[ps], (uint32_t)(((i / STAGES) & 1) ^ 1), status)) break;
+                if (++ps == STAGES) ps = 0;
+            }
+            if (rank == 1) mbar_wait(drain, 0, status);   // (the leader's last commit arrives in both CTAs)
         } else if (warp == 1 && rank == 0) {
             constexpr uint32_t idesc = f8_idesc(256, BN);
             const uint64_t a_desc = smem_desc(smem_u32(tile_a(0)), 16, 1024, 2), b_desc = smem_desc(smem_u32(tile_b(0)), 16, 1024, 2);
-            int s = 0, b = 0;
+            int s = 0, b = 0, it = 0;
             uint32_t ph = 0, bph = 1;   // the first use of each accumulator waits for nothing
             bool ready = false;
-            for (int it = 0; it < total; ++it) {
+            for (; it < total; ++it) {
                 if ((BUFS != 4 || !__all_sync(0xffffffffu, ready)) &&
                     (!f8_warp_wait(&full[s], ph, status) || !f8_warp_wait(&acc_empty[b], bph, status)))
                     break;
@@ -599,6 +605,15 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             if (elect_one()) f8_commit_pair(drain);
             __syncwarp();
             mbar_wait(drain, 0, status);
+            // before this CTA may exit: the promotion warps of both CTAs have given back each accumulator's last sums (the
+            // loop's waits, BUFS blocks on)
+            for (int i = 0; it == total && i < BUFS; ++i) {
+                if (!f8_warp_wait(&acc_empty[b], bph, status)) break;
+                if (++b == BUFS) {
+                    b = 0;
+                    bph ^= 1;
+                }
+            }
         } else if (warp == 2 && lane == 0 && rank == 1) {
             const uint32_t at = f8_mapa(full, 0);
             int s = 0;
@@ -740,8 +755,10 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
-    // Neither CTA frees tensor memory or exits while the pair's MMAs, reads or arrivals may touch it. Relaxed: no data of
-    // the other CTA is read after it, and a release would wait for the stores of y to be performed.
+    // Neither CTA frees tensor memory or exits while the pair's MMAs or reads may touch it. Every arrival from the other CTA
+    // has been waited for above in the one it goes to: at full[] and acc_empty[] by the issuing warp, at empty[] by the
+    // producers, at drain by the issuing warp and the peer's producer, at acc_full[] by the promotion warps. So this barrier
+    // orders no memory and is relaxed (a release would wait for the stores of y to be performed).
     tc_fence_before();
     f8_cluster_arrive_relaxed();
     f8_cluster_wait();
