@@ -284,6 +284,16 @@ GDN_DEV bool mbar_wait(uint64_t *bar, uint32_t parity, int *status) {
     }
 }
 
+// Lane 0 waits (bounded), the whole warp learns the outcome. A shuffle or a vote orders no memory between the lanes;
+// __syncwarp does, so that what lane 0 has seen complete is complete for the others too.
+GDN_DEV bool mbar_wait_lane0(uint64_t *bar, uint32_t parity, int lane, int *status) {
+    bool ok = true;
+    if (lane == 0) ok = mbar_wait(bar, parity, status);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok;
+}
+
 // True in one lane of a whole warp. A warp that issues copies or MMAs runs its loop with all lanes and elects one
 // around the instructions alone: their operands are warp-uniform registers, and from inside a one-lane branch each
 // MMA took about 90 cycles to issue, more than it ran.

@@ -150,13 +150,17 @@ __device__ __forceinline__ bool f8_warp_wait(uint64_t *bar, uint32_t parity, int
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
-// ... on two barriers, the first look at both in one instruction (even lanes at one, odd lanes at the other).
+// ... on two barriers, the first look at both in one instruction (even lanes at one, odd lanes at the other; __syncwarp
+// makes what each half has seen complete so for the other, which the vote does not).
 __device__ __forceinline__ bool f8_warp_wait2(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, int *status) {
     const bool odd = threadIdx.x & 1;
-    if (__all_sync(0xffffffffu, mbar_try_wait(odd ? b1 : b0, odd ? p1 : p0))) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait(odd ? b1 : b0, odd ? p1 : p0))) {
+        __syncwarp();
+        return true;
+    }
     return f8_warp_wait(b0, p0, status) && f8_warp_wait(b1, p1, status);
 }
-// A look at two barriers, which the warp has to agree on.
+// A look at two barriers, which the warp has to agree on (and to __syncwarp after).
 __device__ __forceinline__ bool f8_look2(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1) {
     const bool odd = threadIdx.x & 1;
     uint32_t ok;
@@ -323,13 +327,10 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         }
     } else if (warp < 4) {
         // factors of chunk c (K blocks kChunk c ..) for the tile's rows, rows past M zero
-        bool ok = true;
         const float *bs_row = bs + (int64_t)blockIdx.x * kb_all + kb0;
         for (int c = 0; c * kChunk < nkb; ++c) {
             const int b = c & 1, cnt = min(kChunk, nkb - c * kChunk);
-            if (lane == 0) ok = mbar_wait(&scl_empty[b], (uint32_t)(((c >> 1) & 1) ^ 1), status);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
+            if (!mbar_wait_lane0(&scl_empty[b], (uint32_t)(((c >> 1) & 1) ^ 1), lane, status)) break;
             for (int r = (warp - 2) * 32 + lane; r < MT; r += 64) {
                 const bool live = m0 + r < M;
                 const float *as_row = as + (int64_t)(live ? m0 + r : 0) * kb_all + kb0;
@@ -578,6 +579,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
                 if ((BUFS != 4 || !__all_sync(0xffffffffu, ready)) &&
                     (!f8_warp_wait(&full[s], ph, status) || !f8_warp_wait(&acc_empty[b], bph, status)))
                     break;
+                if constexpr (BUFS == 4) __syncwarp();
                 tc_fence_after();
                 const int s_now = s, b_now = b;
                 if (++s == STAGES) {
