@@ -212,11 +212,16 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 }
             }
             // before the CTA may exit: the latest load armed on each stage has landed (bounded; on
-            // the normal path every one of them was consumed already)
+            // the normal path every one of them was consumed already) ..
             for (int s = 0; s < STAGES && s < it; ++s) {
                 const int last = it - 1 - ((it - 1 - s) % STAGES);   // the last use of stage s
                 mbar_wait(&full[s], (uint32_t)((last / STAGES) & 1), status);
             }
+            // .. the leader's commit of the MMAs that read it has arrived here (the loop's waits, STAGES blocks on), and
+            // in the peer the leader's last commit
+            for (int i = it; ok && i < it + STAGES; ++i)
+                if (!mbar_wait(&empty[i % STAGES], (uint32_t)(((i / STAGES) & 1) ^ 1), status)) break;
+            if (rank == 1) mbar_wait(drain, 0, status);
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
@@ -249,10 +254,8 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 if (ok) tc_commit_pair(acc_full);
             }
             // before the pair may free tensor memory: every MMA issued has completed (bounded)
-            if (it > 0) {
-                tc_commit_pair(drain);
-                mbar_wait(drain, 0, status);
-            }
+            tc_commit_pair(drain);
+            mbar_wait(drain, 0, status);
         }
     } else if (warp >= 4 && warp < 8) {
         const int quarter = warp - 4;
@@ -362,8 +365,8 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         }
     }
 
-    // neither CTA frees tensor memory or exits while the pair's MMAs, reads or remote arrivals
-    // may still touch it
+    // neither CTA frees tensor memory or exits while the pair's MMAs or reads may touch it; the epilogue warps' remote
+    // arrivals are released by it, the commits' have been waited for by the producers
     tc_fence_before();
     cluster_sync_all();
     if (warp == 1) {
