@@ -764,16 +764,18 @@ def gdn_short_conv1d_silu_decode_pooled(x, weight, conv_pool, slots, parts=None,
         _contig(weight, conv_pool, slots, y)
     if y is None:
         y = _new((B, C), _bf, dev, stream, torch.zeros)
+    # the views come first: a call that fails has not shifted the pool
     if parts is None:
         widths, n = None, 0
+        out = y if y.shape == (B, C) else y.view(-1)[:B * C].view(B, C)
     else:
         n = len(parts)
         widths = (ctypes.c_int32 * n)(*parts)
+        fit = not (B and C and n) or (min(parts) >= 0 and sum(parts) == C)
+        out = _conv_planes(parts, B, C, y, x.device)[2] if fit else None   # (the library refuses widths that do not)
     _launch(LIB.gdn_short_conv1d_silu_decode_pooled, dev, stream, x.data_ptr(), ldx, weight.data_ptr(), B, C, K,
             conv_pool.data_ptr(), conv_pool.shape[0], slots.data_ptr(), y.data_ptr(), widths, n)
-    if parts is None:
-        return y if y.shape == (B, C) else y.view(-1)[:B * C].view(B, C)
-    return _conv_planes(parts, B, C, y, x.device)[2]
+    return out
 
 
 INJECT_SKIP_PREP_LOADS = 1

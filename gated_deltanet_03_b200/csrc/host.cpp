@@ -4,8 +4,9 @@
 //
 // Every function either does the whole call and returns its result, or returns None having done nothing: an argument
 // that is not plainly right (type, dtype, device, layout, size), another device than the current one, a status
-// other than GDN_OK. The Python binding then goes its own way, which names what is wrong. No exception leaves a
-// function, no tensor is kept.
+// other than GDN_OK. The Python binding then goes its own way, which names what is wrong. So all that can fail (outputs,
+// their views, the objects of the result) is made before the entry point is called, and nothing after: a call that the
+// binding makes again would advance states in place twice. No exception leaves a function, no tensor is kept.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -95,27 +96,38 @@ bool truth(PyObject *o) {
     need(v >= 0);
     return v != 0;
 }
-void done(gdn_status s) { need(s == GDN_OK); }
+// A new reference (the call is not for this path where there is none), given up with the call that fails.
+class Ref {
+    PyObject *p_;
 
-PyObject *give(PyObject *given, const at::Tensor &x) {
-    if (given != Py_None) {
-        Py_INCREF(given);
-        return given;
+public:
+    explicit Ref(PyObject *p) : p_(p) { need(p != nullptr); }
+    Ref(Ref &&r) noexcept : p_(r.p_) { r.p_ = nullptr; }
+    Ref(const Ref &) = delete;
+    ~Ref() { Py_XDECREF(p_); }
+    PyObject *get() const { return p_; }
+    PyObject *release() {
+        PyObject *p = p_;
+        p_ = nullptr;
+        return p;
     }
-    return THPVariable_Wrap(x);
+};
+// The result of a call whose entry point answered `s`.
+PyObject *done(gdn_status s, Ref &&result) {
+    need(s == GDN_OK);
+    return result.release();
 }
-PyObject *pair(PyObject *a, PyObject *b) {
-    PyObject *t = a && b ? PyTuple_Pack(2, a, b) : nullptr;
-    Py_XDECREF(a);
-    Py_XDECREF(b);
-    return t;
+Ref give(PyObject *given, const at::Tensor &x) {
+    if (given == Py_None) return Ref(THPVariable_Wrap(x));
+    Py_INCREF(given);
+    return Ref(given);
 }
+Ref pair(const Ref &a, const Ref &b) { return Ref(PyTuple_Pack(2, a.get(), b.get())); }
 
 template <typename F>
 PyObject *guarded(F &&f) {
     try {
-        PyObject *r = f();
-        if (r) return r;
+        return f();
     } catch (...) {
     }
     PyErr_Clear();
@@ -141,9 +153,9 @@ PyObject *py_gemm(PyObject *, PyObject *const *a, Py_ssize_t n) {
             need(t == kBf16 || t == kF32);
         }
         const at::Tensor y = out(a[4], dev, t, {M, N});
-        done(lib.gemm(ptr<uint8_t>(aq), ptr<float>(as), ptr<uint8_t>(bq), ptr<float>(bs), M, N, K, t == kBf16 ? GDN_BF16 : GDN_F32,
-                      y.data_ptr(), stream()));
-        return give(a[4], y);
+        Ref r = give(a[4], y);
+        return done(lib.gemm(ptr<uint8_t>(aq), ptr<float>(as), ptr<uint8_t>(bq), ptr<float>(bs), M, N, K,
+                             t == kBf16 ? GDN_BF16 : GDN_F32, y.data_ptr(), stream()), std::move(r));
     });
 }
 
@@ -159,8 +171,9 @@ PyObject *py_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const bool weight = truth(a[3]);
         const int64_t kb = ((int64_t)K + 127) / 128, rows = weight ? ((int64_t)M + 127) / 128 : M;
         const at::Tensor xq = out(a[1], dev, kF8, {M, K}), xs = out(a[2], dev, kF32, {rows, kb});
-        done((weight ? lib.quantize_weight : lib.quantize_act)(x.data_ptr(), ldx, t, M, K, ptr<uint8_t>(xq), ptr<float>(xs), stream()));
-        return pair(give(a[1], xq), give(a[2], xs));
+        Ref r = pair(give(a[1], xq), give(a[2], xs));
+        return done((weight ? lib.quantize_weight : lib.quantize_act)(x.data_ptr(), ldx, t, M, K, ptr<uint8_t>(xq), ptr<float>(xs),
+                                                                      stream()), std::move(r));
     });
 }
 
@@ -178,8 +191,9 @@ PyObject *py_tail(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor &z = whole(tensor(a[1]), dev, o.scalar_type(), M * K), &w = whole(tensor(a[2]), dev, kF32, D);
         const double eps = number(a[3]);
         const at::Tensor xq = out(a[4], dev, kF8, {M, K}), xs = out(a[5], dev, kF32, {M, kb});
-        done(lib.tail(o.data_ptr(), z.data_ptr(), ptr<float>(w), (float)eps, M, Hv, D, t, ptr<uint8_t>(xq), ptr<float>(xs), stream()));
-        return pair(give(a[4], xq), give(a[5], xs));
+        Ref r = pair(give(a[4], xq), give(a[5], xs));
+        return done(lib.tail(o.data_ptr(), z.data_ptr(), ptr<float>(w), (float)eps, M, Hv, D, t, ptr<uint8_t>(xq), ptr<float>(xs),
+                             stream()), std::move(r));
     });
 }
 
@@ -216,25 +230,24 @@ PyObject *py_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 need(t == kBf16 || t == kF32);
             }
             const at::Tensor o = out(a[11], dev, t, {B, Hv, D}, true);
-            done(lib.decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), ga.data_ptr(), gb.data_ptr(), ldg, gt, ptr<float>(A_log),
-                            ptr<float>(dt_bias), B, Hk, Hv, D, D, (float)scale, l2, GDN_BF16, ptr<float>(pool), i32(pool.size(0)),
-                            ptr<int32_t>(slots), o.data_ptr(), t == kBf16 ? GDN_BF16 : GDN_F32, stream()));
-            return give(a[11], o);
+            Ref r = give(a[11], o);
+            return done(lib.decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), ga.data_ptr(), gb.data_ptr(), ldg, gt, ptr<float>(A_log),
+                                   ptr<float>(dt_bias), B, Hk, Hv, D, D, (float)scale, l2, GDN_BF16, ptr<float>(pool),
+                                   i32(pool.size(0)), ptr<int32_t>(slots), o.data_ptr(), t == kBf16 ? GDN_BF16 : GDN_F32, stream()),
+                        std::move(r));
         }
         const at::Tensor &z = on(tensor(a[12]), dev, kBf16), &w = whole(tensor(a[13]), dev, kF32, 128);
         need(z.sizes() == v.sizes() && z.stride(2) == 1 && (Hv <= 1 || z.stride(1) == D));
         const double eps = number(a[14]);
         void *o = a[11] == Py_None ? nullptr : whole(tensor(a[11]), dev, kBf16, v.numel()).data_ptr();
         const at::Tensor xq = out(a[15], dev, kF8, {B, (int64_t)Hv * D}, true), xs = out(a[16], dev, kF32, {B, Hv}, true);
-        done(lib.decode_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), ga.data_ptr(), gb.data_ptr(), ldg, gt, ptr<float>(A_log),
-                            ptr<float>(dt_bias), B, Hk, Hv, D, D, (float)scale, l2, GDN_BF16, ptr<float>(pool), i32(pool.size(0)),
-                            ptr<int32_t>(slots), z.data_ptr(), B > 1 ? z.stride(0) : (int64_t)Hv * D, ptr<float>(w), (float)eps,
-                            ptr<uint8_t>(xq), ptr<float>(xs), o, stream()));
-        PyObject *r0 = give(a[15], xq), *r1 = give(a[16], xs);
-        PyObject *r = r0 && r1 ? PyTuple_Pack(3, r0, r1, a[11]) : nullptr;
-        Py_XDECREF(r0);
-        Py_XDECREF(r1);
-        return r;
+        const Ref r0 = give(a[15], xq), r1 = give(a[16], xs);
+        Ref r(PyTuple_Pack(3, r0.get(), r1.get(), a[11]));
+        return done(lib.decode_fp8(q.data_ptr(), k.data_ptr(), v.data_ptr(), ga.data_ptr(), gb.data_ptr(), ldg, gt, ptr<float>(A_log),
+                                   ptr<float>(dt_bias), B, Hk, Hv, D, D, (float)scale, l2, GDN_BF16, ptr<float>(pool),
+                                   i32(pool.size(0)), ptr<int32_t>(slots), z.data_ptr(), B > 1 ? z.stride(0) : (int64_t)Hv * D,
+                                   ptr<float>(w), (float)eps, ptr<uint8_t>(xq), ptr<float>(xs), o, stream()),
+                    std::move(r));
     });
 }
 
@@ -265,25 +278,23 @@ PyObject *py_conv(PyObject *, PyObject *const *a, Py_ssize_t n) {
             need(sum == C);
         }
         const at::Tensor y = out(a[5], dev, kBf16, {B, C}, true);
-        done(lib.conv(x.data_ptr(), B > 1 ? x.stride(0) : C, ptr<float>(w), B, C, K, pool.data_ptr(), i32(pool.size(0)),
-                      ptr<int32_t>(slots), y.data_ptr(), parts ? widths : nullptr, parts, stream()));
-        if (!parts) {
-            if (y.dim() == 2 && y.size(0) == B && y.size(1) == C) return give(a[5], y);
-            return THPVariable_Wrap(y.view({-1}).narrow(0, 0, (int64_t)B * C).view({B, C}));
-        }
-        const at::Tensor flat = y.view({-1});
-        PyObject *list = PyList_New(parts);
-        int64_t at = 0;
-        for (int32_t p = 0; list && p < parts; ++p) {
-            PyObject *view = THPVariable_Wrap(flat.narrow(0, at, (int64_t)B * widths[p]).view({B, widths[p]}));
-            if (!view) {
-                Py_DECREF(list);
-                return nullptr;
+        auto result = [&]() -> Ref {
+            if (!parts && y.dim() == 2 && y.size(0) == B && y.size(1) == C) return give(a[5], y);
+            const at::Tensor flat = y.view({-1});
+            if (!parts) return Ref(THPVariable_Wrap(flat.narrow(0, 0, (int64_t)B * C).view({B, C})));
+            Ref list(PyList_New(parts));
+            int64_t at = 0;
+            for (int32_t p = 0; p < parts; ++p) {
+                Ref view(THPVariable_Wrap(flat.narrow(0, at, (int64_t)B * widths[p]).view({B, widths[p]})));
+                PyList_SET_ITEM(list.get(), p, view.release());
+                at += (int64_t)B * widths[p];
             }
-            PyList_SET_ITEM(list, p, view);
-            at += (int64_t)B * widths[p];
-        }
-        return list;
+            return list;
+        };
+        Ref r = result();
+        return done(lib.conv(x.data_ptr(), B > 1 ? x.stride(0) : C, ptr<float>(w), B, C, K, pool.data_ptr(), i32(pool.size(0)),
+                             ptr<int32_t>(slots), y.data_ptr(), parts ? widths : nullptr, parts, stream()),
+                    std::move(r));
     });
 }
 
