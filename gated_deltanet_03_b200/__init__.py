@@ -16,6 +16,7 @@ Functions keep the C names:
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 
 import torch
@@ -524,13 +525,24 @@ def gdn_short_conv1d_silu_decode(x, weight, conv_state, parts=None, y=None, stre
 # built, are made from here, each checking its tensors in one pass (_ok) and going through the named checks above
 # only to say what is wrong.
 
-try:
-    from . import _gdn_host as _host
-    _host.bind(*[ctypes.cast(getattr(LIB, n), ctypes.c_void_p).value for n in (
+
+def _load_host():
+    """The compiled host path, or None where it is not built or was built from other sources or for another torch (its
+    calls would then hand the library shifted arguments, or read a tensor's fields in the wrong places)."""
+    try:
+        from .build import host_key
+        host = importlib.import_module("._gdn_host", __name__)
+        if host.KEY != host_key(torch.__version__):
+            return None
+    except (ImportError, AttributeError, OSError):
+        return None
+    host.bind(*[ctypes.cast(getattr(LIB, n), ctypes.c_void_p).value for n in (
         "fp8_gemm", "fp8_quantize_act", "fp8_quantize_weight", "gdn_gated_rmsnorm_silu_fp8", "gdn_decode_step_pooled",
         "gdn_decode_step_pooled_gated_fp8", "gdn_short_conv1d_silu_decode_pooled")])
-except ImportError:
-    _host = None
+    return host
+
+
+_host = _load_host()
 
 _F8, _BF = (torch.float8_e4m3fn,), (torch.bfloat16,)
 _f8, _bf, _f32, _i32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32

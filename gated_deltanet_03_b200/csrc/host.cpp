@@ -332,4 +332,15 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdn_host", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__gdn_host() { return PyModule_Create(&module); }
+#ifndef GDN_HOST_KEY   // what this file was built from and for (build.py)
+#define GDN_HOST_KEY ""
+#endif
+
+PyMODINIT_FUNC PyInit__gdn_host() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "KEY", GDN_HOST_KEY) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
