@@ -37,7 +37,8 @@ ABI_SYMBOLS = (
     "fp8_quantize_act", "fp8_quantize_weight", "gdn_gated_rmsnorm_silu_fp8", "fp8_gemm",
     "gdn_decode_step_pooled", "gdn_decode_step_pooled_gated_fp8",
     "gdn_short_conv1d_silu", "gdn_short_conv1d_silu_decode", "gdn_short_conv1d_silu_decode_pooled",
-    "gdn_prefill_chunked_static_ws", "gdn_get_device_status", "gdn_debug_set_wait", "gdn_status_string",
+    "gdn_prefill_chunked_static_ws", "gdn_get_device_status", "gdn_debug_set_wait", "gdn_debug_fp8_gemm",
+    "gdn_debug_fp8_gemm_form", "gdn_status_string",
     "gdn_version",
 )
 
@@ -91,6 +92,8 @@ def _load() -> ctypes.CDLL:
     lib.gdn_short_conv1d_silu_decode_pooled.argtypes = [P, i64, P, i32, i32, i32, P, i32, P, P, P, i32, P]
     lib.gdn_get_device_status.argtypes = [P]
     lib.gdn_debug_set_wait.argtypes = [ctypes.c_uint64, ctypes.c_uint32]
+    lib.gdn_debug_fp8_gemm.argtypes = [P, P, P, P, i32, i32, i32, i32, P, i32, i32, P]
+    lib.gdn_debug_fp8_gemm_form.argtypes = [i32, i32, i32, P, P, P]
     lib.gdn_status_string.argtypes = [i32]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_version.restype = i32
@@ -101,7 +104,8 @@ def _load() -> ctypes.CDLL:
                  "nvfp4_gemm_colscale", "nvfp4_fused_col_alpha", "q4k_gemm",
                  "fp8_quantize_act", "fp8_quantize_weight", "gdn_gated_rmsnorm_silu_fp8", "fp8_gemm",
                  "gdn_decode_step_pooled", "gdn_decode_step_pooled_gated_fp8", "gdn_short_conv1d_silu_decode_pooled",
-                 "gdn_short_conv1d_silu", "gdn_short_conv1d_silu_decode", "gdn_get_device_status", "gdn_debug_set_wait"):
+                 "gdn_short_conv1d_silu", "gdn_short_conv1d_silu_decode", "gdn_get_device_status", "gdn_debug_set_wait",
+                 "gdn_debug_fp8_gemm", "gdn_debug_fp8_gemm_form"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -797,6 +801,33 @@ def gdn_debug_set_wait(wait_limit_ns: int = 0, inject_flags: int = 0) -> None:
     """Test support: bounded-wait limit (0 = the default 1 s) and the switches that make a wait
     run out with nothing in flight (INJECT_SKIP_PREP_LOADS) on the current device."""
     _check("gdn_debug_set_wait", LIB.gdn_debug_set_wait(int(wait_limit_ns), int(inject_flags)))
+
+
+# The forms of fp8_gemm by number: (kernel, tile rows or columns).
+FP8_GEMM_FORMS = (("narrow", 16), ("narrow", 32), ("narrow", 64), ("narrow", 128), ("wide", 128), ("wide", 192), ("wide", 256))
+
+
+def gdn_debug_fp8_gemm(aq, as_, bq, bs, form: int, split: int = 1, out_dtype=torch.bfloat16, y=None, stream=None):
+    """Test support: fp8_gemm in a given form (FP8_GEMM_FORMS) and split of K."""
+    (M, K), N = aq.shape, bq.shape[0]
+    kb = (K + 127) // 128
+    _args(aq.device, aq=(aq, _F8, None), as_=(as_, _F32, M * kb), bq=(bq, _F8, N * K), bs=(bs, _F32, (N + 127) // 128 * kb),
+          y=(y, _IO, M * N))
+    if y is None:
+        y = torch.empty((M, N), dtype=out_dtype, device=aq.device)
+    _contig(aq, as_, bq, bs, y)
+    st = LIB.gdn_debug_fp8_gemm(_ptr(aq), _ptr(as_), _ptr(bq), _ptr(bs), M, N, K, _dt(y), _ptr(y), form, split, _stream(stream))
+    _check("gdn_debug_fp8_gemm", st)
+    return y
+
+
+def gdn_debug_fp8_gemm_form(M: int, N: int, K: int, device=None):
+    """Test support: (form, split) that fp8_gemm picks, on the current device or on one that runs device = (SMs, clusters
+    of 2, 4 and 8 CTAs, SM pairs) at once."""
+    numbers = None if device is None else (ctypes.c_int32 * 5)(*device)
+    form, split = ctypes.c_int32(), ctypes.c_int32()
+    _check("gdn_debug_fp8_gemm_form", LIB.gdn_debug_fp8_gemm_form(M, N, K, numbers, ctypes.byref(form), ctypes.byref(split)))
+    return form.value, split.value
 
 
 def gdn_get_device_status(stream=None) -> int:

@@ -355,8 +355,9 @@ gdn_status gdn_gated_rmsnorm_silu_fp8(const void *o, const void *z, const float 
     return launched(gdn::launch_gated_rmsnorm_fp8(t, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-gdn_status fp8_gemm(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs, int32_t M, int32_t N,
-                    int32_t K, gdn_dtype out_dtype, void *y, gdn_stream_t stream) {
+// form < 0: the one that the library picks.
+static gdn_status fp8_gemm_in(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs, int32_t M, int32_t N,
+                              int32_t K, gdn_dtype out_dtype, void *y, int32_t form, int32_t split, gdn_stream_t stream) {
     if (M < 0 || N < 0 || K < 0 || !dtype_ok(out_dtype)) return GDN_ERR_INVALID_ARG;
     if (K % 16 != 0 || N % 16 != 0 || M > 128 * 65535 || K > INT32_MAX - 255 || N > INT32_MAX - 255)
         return GDN_ERR_UNSUPPORTED;
@@ -365,7 +366,38 @@ gdn_status fp8_gemm(const uint8_t *aq, const float *as, const uint8_t *bq, const
     if (!aq || !as || !bq || !bs || !y) return GDN_ERR_INVALID_ARG;
     if (!aligned16(aq) || !aligned16(bq) || !aligned16(y)) return GDN_ERR_INVALID_ARG;
     gdn::Fp8GemmArgs g{aq, as, bq, bs, M, N, K, out_dtype == GDN_BF16, y, status_ptr()};
-    return launched(gdn::launch_fp8_gemm(g, reinterpret_cast<cudaStream_t>(stream)));
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (form < 0) return launched(gdn::launch_fp8_gemm(g, st));
+    gdn::Fp8Device dev;
+    if (gdn::fp8_device(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+    if (!gdn::fp8_form_ok(M, N, K, {form, split}, dev)) return GDN_ERR_UNSUPPORTED;
+    return launched(gdn::launch_fp8_gemm_form(g, {form, split}, dev, st));
+}
+
+gdn_status fp8_gemm(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs, int32_t M, int32_t N,
+                    int32_t K, gdn_dtype out_dtype, void *y, gdn_stream_t stream) {
+    return fp8_gemm_in(aq, as, bq, bs, M, N, K, out_dtype, y, -1, 1, stream);
+}
+
+gdn_status gdn_debug_fp8_gemm(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs, int32_t M, int32_t N,
+                              int32_t K, gdn_dtype out_dtype, void *y, int32_t form, int32_t split, gdn_stream_t stream) {
+    if (form < 0 || form >= gdn::kFp8Forms) return GDN_ERR_INVALID_ARG;
+    return fp8_gemm_in(aq, as, bq, bs, M, N, K, out_dtype, y, form, split, stream);
+}
+
+gdn_status gdn_debug_fp8_gemm_form(int32_t M, int32_t N, int32_t K, const int32_t *device, int32_t *form, int32_t *split) {
+    if (M < 1 || N < 1 || K < 1 || !form || !split) return GDN_ERR_INVALID_ARG;
+    gdn::Fp8Device dev;
+    if (device) {
+        dev = {device[0], {0, device[1], device[2], device[3]}, device[4]};
+        if (dev.sms < 1 || dev.pairs < 1) return GDN_ERR_INVALID_ARG;
+    } else if (gdn::fp8_device(&dev) != cudaSuccess) {
+        return GDN_ERR_CUDA;
+    }
+    const gdn::Fp8Form f = gdn::fp8_gemm_form(M, N, K, dev);
+    *form = f.form;
+    *split = f.split;
+    return GDN_OK;
 }
 
 static gdn_status pooled_decode(gdn::PooledDecodeArgs &d, int32_t Dk, int32_t Dv, gdn_dtype gate_dtype,

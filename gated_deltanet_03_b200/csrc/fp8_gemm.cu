@@ -816,11 +816,6 @@ bool f8_map_out(CUtensorMap *m, void *ptr, uint64_t M, uint64_t N, bool bf16) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// What the device runs at once: SMs, clusters of 2, 4 and 8 CTAs (a cluster lies within one GPC, so fewer than the
-// SMs allow; the query counts one CTA an SM), SM pairs of the wide kernel. Kernel attributes are set alongside.
-struct Fp8Device {
-    int sms, clusters[4], pairs;
-};
 template <typename K>
 cudaError_t f8_count_clusters(K kernel, int threads, int smem, dim3 cluster, int *count) {
     cudaLaunchConfig_t cfg = {};
@@ -846,29 +841,6 @@ cudaError_t f8_set_wide() {
     const cudaError_t e = cudaFuncSetAttribute(fp8_gemm_wide_kernel<BN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideCfg<BN>::SMEM);
     return e != cudaSuccess ? e : cudaFuncSetAttribute(fp8_gemm_wide_kernel<BN, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, WideCfg<BN>::SMEM);
 }
-cudaError_t f8_device(Fp8Device *out) {
-    static PerDevice<Fp8Device> rec;
-    return rec.get(
-        [](int dev, Fp8Device &r) {
-            cudaError_t e = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev);
-            if (e == cudaSuccess) e = f8_set_narrow<16>();
-            if (e == cudaSuccess) e = f8_set_narrow<32>();
-            if (e == cudaSuccess) e = f8_set_narrow<64>();
-            if (e == cudaSuccess) e = f8_set_narrow<128>();
-            if (e == cudaSuccess) e = f8_set_wide<128>();
-            if (e == cudaSuccess) e = f8_set_wide<192>();
-            if (e == cudaSuccess) e = f8_set_wide<256>();
-            for (int i = 1; i < 4 && e == cudaSuccess; ++i)
-                e = f8_count_clusters(fp8_gemm_narrow_kernel<128, true>, NarrowCfg<128>::THREADS, NarrowCfg<128>::SMEM,
-                                      dim3(1, 1, 1u << i), &r.clusters[i]);
-            if (e == cudaSuccess)
-                e = f8_count_clusters(fp8_gemm_wide_kernel<256, true>, WideCfg<256>::THREADS, WideCfg<256>::SMEM, dim3(2), &r.pairs);
-            if (e == cudaSuccess && r.pairs < 1) e = cudaErrorInvalidConfiguration;
-            return e;
-        },
-        out);
-}
-
 template <int MT>
 cudaError_t launch_narrow(const Fp8GemmArgs &g, int split, cudaStream_t st) {
     using Cfg = NarrowCfg<MT>;
@@ -922,7 +894,48 @@ cudaError_t launch_wide(const Fp8GemmArgs &g, int pairs, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, fp8_gemm_wide_kernel<BN, false>, ma, mb, my, g.as, g.bs, g.M, g.N, kb, g.status);
 }
 
+struct Cost {
+    int tile;
+    float start, end, block, push;   // push: what a split's exchange of partial sums adds
+};
+constexpr Cost kCost[kFp8Forms] = {{16, 2.1f, 1.0f, 0.26f, 0.4f},   {32, 2.2f, 1.0f, 0.285f, 0.9f},  {64, 2.7f, 1.0f, 0.31f, 1.1f},
+                                   {128, 3.6f, 1.0f, 0.42f, 2.3f},  {128, 3.1f, 0.8f, 0.285f, 0.0f}, {192, 3.7f, 1.0f, 0.36f, 0.0f},
+                                   {256, 4.0f, 1.2f, 0.415f, 0.0f}};
+
 }  // namespace
+
+cudaError_t fp8_device(Fp8Device *out) {
+    static PerDevice<Fp8Device> rec;
+    return rec.get(
+        [](int dev, Fp8Device &r) {
+            cudaError_t e = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev);
+            if (e == cudaSuccess) e = f8_set_narrow<16>();
+            if (e == cudaSuccess) e = f8_set_narrow<32>();
+            if (e == cudaSuccess) e = f8_set_narrow<64>();
+            if (e == cudaSuccess) e = f8_set_narrow<128>();
+            if (e == cudaSuccess) e = f8_set_wide<128>();
+            if (e == cudaSuccess) e = f8_set_wide<192>();
+            if (e == cudaSuccess) e = f8_set_wide<256>();
+            for (int i = 1; i < 4 && e == cudaSuccess; ++i)
+                e = f8_count_clusters(fp8_gemm_narrow_kernel<128, true>, NarrowCfg<128>::THREADS, NarrowCfg<128>::SMEM,
+                                      dim3(1, 1, 1u << i), &r.clusters[i]);
+            if (e == cudaSuccess)
+                e = f8_count_clusters(fp8_gemm_wide_kernel<256, true>, WideCfg<256>::THREADS, WideCfg<256>::SMEM, dim3(2), &r.pairs);
+            if (e == cudaSuccess && r.pairs < 1) e = cudaErrorInvalidConfiguration;
+            return e;
+        },
+        out);
+}
+
+bool fp8_form_ok(int64_t M, int64_t N, int64_t K, Fp8Form f, const Fp8Device &dev) {
+    if (f.form < 0 || f.form >= kFp8Forms) return false;
+    if (f.form >= kFp8Narrow) return f.split == 1;
+    if ((M + kCost[f.form].tile - 1) / kCost[f.form].tile > 65535) return false;   // grid y
+    if (f.split == 1) return true;
+    // a cluster of that size runs, and every CTA has a K block
+    const int lg = f.split == 2 ? 1 : f.split == 4 ? 2 : f.split == 8 ? 3 : 0;
+    return lg && dev.clusters[lg] > 0 && (K + 127) / 128 >= f.split;
+}
 
 // The kernel and tile with the least estimated time: a start, and per wave of CTAs (or pairs) an end and a cost for
 // each K block, in us at 1965 MHz. Fitted to timings of each form at 1 to 64 K blocks (bf16 output, CUDA-graph
@@ -932,60 +945,60 @@ cudaError_t launch_wide(const Fp8GemmArgs &g, int pairs, cudaStream_t st) {
 // For example (us: narrow 64, narrow 128, wide 128, wide 192, wide 256)
 //     256 x 2048 x 4096   10.2, 13.2, 12.4, 15.7, 17.7      1024 x 2048 x 4096   26.0, 18.6, 13.5, 16.6, 18.8
 //     128 x 2048 x 4096    8.1, 10.7, 12.3, 15.4, 17.6      256 x 12352 x 2048   24.3, 21.2, 13.8, 10.9, 12.5
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st) {
-    Fp8Device dev;
-    const cudaError_t e = f8_device(&dev);
-    if (e != cudaSuccess) return e;
-    const int kb = (g.K + 127) / 128;
-    struct Form {
-        int tile;
-        float start, end, block, push;   // push: what a split's exchange of partial sums adds
-    };
-    static const Form narrow[4] = {{16, 2.1f, 1.0f, 0.26f, 0.4f}, {32, 2.2f, 1.0f, 0.285f, 0.9f}, {64, 2.7f, 1.0f, 0.31f, 1.1f},
-                                   {128, 3.6f, 1.0f, 0.42f, 2.3f}};
-    static const Form wide[3] = {{128, 3.1f, 0.8f, 0.285f, 0.0f}, {192, 3.7f, 1.0f, 0.36f, 0.0f}, {256, 4.0f, 1.2f, 0.415f, 0.0f}};
+Fp8Form fp8_gemm_form(int64_t M, int64_t N, int64_t K, const Fp8Device &dev) {
+    const int64_t kb = (K + 127) / 128, nt = (N + 127) / 128;
     float best = 3.0e38f;
-    int form = 0, split = 1;
-    const int64_t nt = (g.N + 127) / 128;
-    for (int i = 0; i < 4; ++i) {
-        const int64_t mt = (g.M + narrow[i].tile - 1) / narrow[i].tile, ctas = nt * mt;
-        if (mt > 65535) continue;   // grid y
+    Fp8Form pick{kFp8Forms - 1, 1};
+    for (int i = 0; i < kFp8Narrow; ++i) {
+        const Cost &c = kCost[i];
+        const int64_t ctas = nt * ((M + c.tile - 1) / c.tile);
         // K split while all clusters run at once and every CTA keeps two K blocks
-        const int per_sm = narrow[i].tile <= 32 ? 2 : 1;
+        const int per_sm = c.tile <= 32 ? 2 : 1;
         for (int lg = 0; lg < 4; ++lg) {
             if (lg && (ctas << lg > (int64_t)per_sm * dev.sms || ctas > (int64_t)per_sm * dev.clusters[lg] || kb < 2 << lg)) break;
+            if (!fp8_form_ok(M, N, K, {i, 1 << lg}, dev)) break;
             // of two CTAs on one SM a K block each takes 1.6 times as long as one alone, and they start later
             const bool two = per_sm == 2 && ctas << lg > dev.sms;
             const int64_t at_once = two ? 2 * dev.sms : dev.sms, waves = ((ctas << lg) + at_once - 1) / at_once;
-            const float block = two ? 1.6f * narrow[i].block : narrow[i].block;
-            const float t = narrow[i].start + (float)waves * (narrow[i].end + (float)((kb + (1 << lg) - 1) >> lg) * block) +
-                            (lg ? narrow[i].push : 0.0f) + (two ? 1.0f : 0.0f);
+            const float block = two ? 1.6f * c.block : c.block;
+            const float t = c.start + (float)waves * (c.end + (float)((kb + (1 << lg) - 1) >> lg) * block) + (lg ? c.push : 0.0f) +
+                            (two ? 1.0f : 0.0f);
             if (t < best) {
                 best = t;
-                form = i;
-                split = 1 << lg;
+                pick = {i, 1 << lg};
             }
         }
-        if (narrow[i].tile >= g.M) break;   // wider tiles hold nothing more
+        if (c.tile >= M) break;   // wider tiles hold nothing more
     }
-    for (int i = 0; i < 3 && g.M > 64; ++i) {
-        const int64_t tiles = (int64_t)((g.N + wide[i].tile - 1) / wide[i].tile) * ((g.M + 255) / 256);
+    for (int i = kFp8Narrow; i < kFp8Forms && M > 64; ++i) {
+        const Cost &c = kCost[i];
+        const int64_t tiles = (N + c.tile - 1) / c.tile * ((M + 255) / 256);
         const int64_t waves = (tiles + dev.pairs - 1) / dev.pairs;
-        const float t = wide[i].start + (float)waves * (wide[i].end + (float)kb * wide[i].block);
+        const float t = c.start + (float)waves * (c.end + (float)kb * c.block);
         if (t < best) {
             best = t;
-            form = 4 + i;
+            pick = {i, 1};
         }
     }
-    switch (form) {
-        case 0: return launch_narrow<16>(g, split, st);
-        case 1: return launch_narrow<32>(g, split, st);
-        case 2: return launch_narrow<64>(g, split, st);
-        case 3: return launch_narrow<128>(g, split, st);
+    return pick;
+}
+
+cudaError_t launch_fp8_gemm_form(const Fp8GemmArgs &g, Fp8Form f, const Fp8Device &dev, cudaStream_t st) {
+    switch (f.form) {
+        case 0: return launch_narrow<16>(g, f.split, st);
+        case 1: return launch_narrow<32>(g, f.split, st);
+        case 2: return launch_narrow<64>(g, f.split, st);
+        case 3: return launch_narrow<128>(g, f.split, st);
         case 4: return launch_wide<128>(g, dev.pairs, st);
         case 5: return launch_wide<192>(g, dev.pairs, st);
         default: return launch_wide<256>(g, dev.pairs, st);
     }
+}
+
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st) {
+    Fp8Device dev;
+    const cudaError_t e = fp8_device(&dev);
+    return e != cudaSuccess ? e : launch_fp8_gemm_form(g, fp8_gemm_form(g.M, g.N, g.K, dev), dev, st);
 }
 
 }  // namespace gdn

@@ -197,7 +197,25 @@ struct Fp8GemmArgs {
     void *y;
     int *status;
 };
+// How the product is done: narrow tiles of 16, 32, 64 or 128 activation rows (forms 0 to 3) with K split over `split`
+// CTAs, or SM pairs on wide tiles of 128, 192 or 256 columns (forms 4 to 6).
+constexpr int kFp8Narrow = 4, kFp8Forms = 7;
+struct Fp8Form {
+    int form, split;
+};
+// What a device runs at once: SMs, clusters of 2, 4 and 8 CTAs (a cluster lies within one GPC, so fewer than the
+// SMs allow; the query counts one CTA an SM), SM pairs of the wide kernel.
+struct Fp8Device {
+    int sms, clusters[4], pairs;
+};
+// This device's numbers (kernel attributes are set alongside).
+cudaError_t fp8_device(Fp8Device *out);
+// Whether a form can do the sizes; the one with the least estimated time.
+bool fp8_form_ok(int64_t M, int64_t N, int64_t K, Fp8Form f, const Fp8Device &dev);
+Fp8Form fp8_gemm_form(int64_t M, int64_t N, int64_t K, const Fp8Device &dev);
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs &g, cudaStream_t st);
+// .. in a given form, which has to be able to do it
+cudaError_t launch_fp8_gemm_form(const Fp8GemmArgs &g, Fp8Form f, const Fp8Device &dev, cudaStream_t st);
 
 // One decode token per row (d = 128, bf16) on states in a pool of slots; with xq set, the gated tail in FP8.
 struct PooledDecodeArgs {

@@ -440,6 +440,19 @@ GDN_API gdn_status gdn_get_device_status(gdn_stream_t stream);
 #define GDN_INJECT_SKIP_PREP_LOADS 1u
 GDN_API gdn_status gdn_debug_set_wait(uint64_t wait_limit_ns, uint32_t inject_flags);
 
+/* Test support for fp8_gemm, which picks one of its kernels' forms by an estimate of their times: 0 to 3 are tiles of
+ * 16, 32, 64 and 128 activation rows with K split over `split` CTAs (1, 2, 4 or 8), 4 to 6 SM pairs on tiles of 256
+ * rows x 128, 192 and 256 columns (split 1).
+ * gdn_debug_fp8_gemm: the product in the form given; GDN_ERR_UNSUPPORTED where that form cannot do it (more than
+ *   65535 tiles of rows in forms 0 to 3, fewer than `split` blocks of K).
+ * gdn_debug_fp8_gemm_form: the form that fp8_gemm picks on a device that runs device[0] SMs, device[1 .. 3] clusters of
+ *   2, 4 and 8 CTAs and device[4] SM pairs at once (host memory; NULL: the current device), without any launch. */
+GDN_API gdn_status gdn_debug_fp8_gemm(const uint8_t *aq, const float *as, const uint8_t *bq, const float *bs, int32_t M,
+                                      int32_t N, int32_t K, gdn_dtype out_dtype, void *y, int32_t form, int32_t split,
+                                      gdn_stream_t stream);
+GDN_API gdn_status gdn_debug_fp8_gemm_form(int32_t M, int32_t N, int32_t K, const int32_t *device, int32_t *form,
+                                           int32_t *split);
+
 /* Static description of a status code. */
 GDN_API const char *gdn_status_string(gdn_status s);
 
