@@ -563,6 +563,13 @@ def _ok(dev, *checks) -> bool:
     return True
 
 
+def _fit(**sizes) -> None:
+    """Sizes that the library takes as 32-bit numbers (ctypes would pass on their lowest bits)."""
+    for name, n in sizes.items():
+        if n > 0x7FFFFFFF:
+            raise ValueError("%s = %d is more than the library takes" % (name, n))
+
+
 def _launch(fn, dev, stream, *args):
     """The library call `fn` on `stream` (default: the device's current stream) with device `dev` current."""
     if stream is None:
@@ -601,6 +608,7 @@ def _fp8_quantize(fn, x, xq, xs, per_row, stream):
         raise ValueError("x must be a 2-D tensor")
     ldx = _row_stride("x", x)
     M, K = x.shape
+    _fit(rows=M, K=K)
     kb = (K + 127) // 128
     rows = M if per_row else (M + 127) // 128
     dev = x.get_device()
@@ -645,6 +653,7 @@ def fp8_gemm(aq, as_, bq, bs, out_dtype=torch.bfloat16, y=None, stream=None):
             return r
     M, K = aq.shape
     N, Kb = bq.shape
+    _fit(M=M, N=N, K=K)
     kb = (K + 127) // 128
     dev = aq.get_device()
     if not (_ok(dev, (aq, _f8, 0), (as_, _f32, M * kb), (bq, _f8, 0), (bs, _f32, (N + 127) // 128 * kb))
@@ -667,6 +676,7 @@ def gdn_gated_rmsnorm_silu_fp8(o, z, weight, eps: float = 1e-6, xq=None, xs=None
         if r is not None:
             return r
     M, Hv, D = o.shape
+    _fit(M=M, Hv=Hv, D=D)
     K = Hv * D
     kb = (K + 127) // 128
     dev, dt = o.get_device(), o.dtype
@@ -689,6 +699,7 @@ def _pooled_sizes(q, k, v, a, b, A_log, dt_bias, state_pool, slots):
     Hv = v.shape[1]
     if a is None or b is None or state_pool is None or slots is None:
         raise ValueError("a, b, state_pool and slots are required")
+    _fit(B=B, Hk=Hk, Hv=Hv, D=D, num_slots=state_pool.shape[0])
     if state_pool.shape[1:] != (Hv, D, D):
         raise ValueError("state_pool must be [num_slots, %d, %d, %d]" % (Hv, D, D))
     if a.shape != (B, Hv) or b.shape != a.shape or v.shape != (B, Hv, D) or k.shape != q.shape:
@@ -772,6 +783,7 @@ def gdn_short_conv1d_silu_decode_pooled(x, weight, conv_pool, slots, parts=None,
     K = weight.shape[1]
     if conv_pool is None or slots is None:
         raise ValueError("conv_pool and slots are required")
+    _fit(B=B, C=C, K=K, num_slots=conv_pool.shape[0])
     if conv_pool.shape[1:] != (K - 1, C) or weight.shape[0] != C:
         raise ValueError("conv_pool must be [num_slots, %d, %d] and weight [%d, K]" % (K - 1, C, C))
     dev = x.get_device()
