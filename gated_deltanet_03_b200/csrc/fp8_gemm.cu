@@ -30,15 +30,17 @@
 //   warp 3     the factors as[m, B] bs[n / 128, B], through shared memory;
 //   warps 4-   (BN / 16 promotion warps) one token row and 64 columns per thread, in fp32 registers (at BN = 256 the
 //              register split by setmaxnreg is 128 x 64 + 512 x 104 = 640 x 96, the launch's own total).
-// A K block of a 256-wide tile takes 840 cycles: the MMAs alone 512, with their signals and loads 620, and the read-back,
-// which shares tensor memory with them, the rest (reading 128 x 256 sums flat out slows a group of MMAs by 28 %).
-// One of a 128-wide tile takes 535, the MMAs alone 256: its 24 KB of loads come at 46 bytes a cycle (a TMA load path
-// measured at about 50), and the signals between the warps alone take 350.
+// A K block of a 256-wide tile takes 815 cycles: the MMAs alone 512, with their signals and loads 620, and the read-back,
+// which shares tensor memory with them, the rest (reading 128 x 256 sums flat out slows a group of MMAs by 28 %). From a
+// tile's last K block to the next tile's first it is 3,260 cycles, 2,220 of them the way of the sums to y.
+// One of a 128-wide tile takes 535, the MMAs alone 256: its 24 KB of loads, at 46 bytes a cycle (a TMA load path
+// measured at about 50), are 520 of them; the signals between the warps alone take 350. A 192-wide tile's 28 KB are 610
+// of 700. So below 256 columns it is the loads that set the pace.
 // With the accumulators neither read back nor added a call of 8192 x 2048 x 4096 takes 58 us instead of 70, without its
 // MMAs 60, with a third of its loads 68: at 256 columns it is the way from an accumulator's MMAs through its promotion to
 // the next ones, with two accumulators in turn, that sets the pace.
-// 32768 x 2048 x 4096: 245 us in a burst (2.24 PFLOP/s), 262 to 284 us back to back, where the 1 kW limit holds the SMs at
-// 1.5 GHz.
+// 32768 x 2048 x 4096 takes 400,000 cycles: 244 us for a call after idle (2.25 PFLOP/s; the SMs at 1.64 GHz already), 268 to
+// 284 us back to back, where the 1 kW limit holds them at 1.4 to 1.5 GHz.
 //
 // Every barrier wait is bounded (gdn_debug_set_wait); an expired one records GDN_ERR_TIMEOUT, issued copies
 // and MMAs are waited for (bounded), tensor memory is freed and the CTA ends.

@@ -7,7 +7,7 @@
 // HBM-bound: 128 KB of state traffic and about 8 operations a state value per (row, head) item. The grid has one
 // CTA per unit of one or more heads of a row; those that run take over the units of CTAs that have not been
 // launched yet (cluster launch control), so each SM does as many as its share of the memory rate allows (equal
-// shares left the fastest SMs idle for a fifth of the time: 188 us against 166 for 256 rows x 32 heads). A
+// shares left the fastest SMs idle for a fifth of the time: 183 us against 166 for 250 live rows x 32 heads). A
 // producer warp brings each item's 64 KB state and its q, k, v, z rows into a ring by bulk copies, so loads
 // stay in flight while items are computed, written back and encoded:
 //   warps 0-15   the state from the stage into registers (8 lanes a row, 2 rows a thread, in the arithmetic of
@@ -21,6 +21,8 @@
 // without a wait or a store: it brings the loop's code into the SM's instruction cache while the first state is on
 // its way. Without it a CTA's first item took 12,700 cycles from its state's arrival to its codes, later ones a
 // third of that, which is most of a small batch's time.
+// 250 live rows x 32 heads take 161.3 us plain and 162.0 with the tail (the bytes at the measured copy rate: 161), 3 live
+// rows x 16 heads 4.9 and 5.1.
 // A row with a negative slot is passed over (its outputs stay as they are); so is a row whose slot is not
 // below num_slots or is named by an earlier row, and the status word then reads GDN_ERR_INVALID_ARG.
 // Every wait is bounded; an expired one records GDN_ERR_TIMEOUT and the warp ends.
