@@ -284,14 +284,13 @@ GDN_DEV bool mbar_wait(uint64_t *bar, uint32_t parity, int *status) {
     }
 }
 
-// Lane 0 waits (bounded), the whole warp learns the outcome. A shuffle or a vote orders no memory between the lanes;
-// __syncwarp does, so that what lane 0 has seen complete is complete for the others too.
-GDN_DEV bool mbar_wait_lane0(uint64_t *bar, uint32_t parity, int lane, int *status) {
-    bool ok = true;
-    if (lane == 0) ok = mbar_wait(bar, parity, status);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
-    return ok;
+// The whole warp waits (bounded), every lane for itself: one lane's wait, passed on by a shuffle or a vote, orders no memory
+// for the others without a __syncwarp after it, and that takes longer. False in every lane if any lane's wait ran out.
+// The first look is apart from the bounded loop: with it a wait for a phase that is over takes 60 cycles, through the
+// loop's code 120.
+GDN_DEV bool mbar_wait_warp(uint64_t *bar, uint32_t parity, int *status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
 }
 
 // True in one lane of a whole warp. A warp that issues copies or MMAs runs its loop with all lanes and elects one

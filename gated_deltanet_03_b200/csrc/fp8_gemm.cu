@@ -146,13 +146,7 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[N]) {
 __device__ __forceinline__ void f8_tmem_ld(uint32_t at, uint32_t (&d)[16]) { tmem_ld16(at, d); }
 __device__ __forceinline__ void f8_tmem_ld(uint32_t at, uint32_t (&d)[32]) { tmem_ld32(at, d); }
 
-// The whole warp waits (bounded); false in every lane if any lane's wait ran out. The first look is apart from
-// the bounded loop: with it a wait for a phase that is over takes 60 cycles, through the loop's code 120.
-__device__ __forceinline__ bool f8_warp_wait(uint64_t *bar, uint32_t parity, int *status) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
-}
-// ... on two barriers, the first look at both in one instruction (even lanes at one, odd lanes at the other; __syncwarp
+// mbar_wait_warp on two barriers, the first look at both in one instruction (even lanes at one, odd lanes at the other; __syncwarp
 // makes what each half has seen complete so for the other, which the vote does not).
 __device__ __forceinline__ bool f8_warp_wait2(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, int *status) {
     const bool odd = threadIdx.x & 1;
@@ -160,7 +154,7 @@ __device__ __forceinline__ bool f8_warp_wait2(uint64_t *b0, uint32_t p0, uint64_
         __syncwarp();
         return true;
     }
-    return f8_warp_wait(b0, p0, status) && f8_warp_wait(b1, p1, status);
+    return mbar_wait_warp(b0, p0, status) && mbar_wait_warp(b1, p1, status);
 }
 // A look at two barriers, which the warp has to agree on (and to __syncwarp after).
 __device__ __forceinline__ bool f8_look2(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1) {
@@ -282,7 +276,7 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     if (warp == 0) {
         int i = 0;
         for (int s = 0, ph = 1; i < nkb; ++i) {
-            if (!f8_warp_wait(&empty[s], (uint32_t)ph, status)) break;
+            if (!mbar_wait_warp(&empty[s], (uint32_t)ph, status)) break;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&full[s], Cfg::STAGE_BYTES);
                 tma_load_2d(tile_w(s), &map_w, &full[s], (kb0 + i) * 128, n0);
@@ -332,7 +326,7 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         const float *bs_row = bs + (int64_t)blockIdx.x * kb_all + kb0;
         for (int c = 0; c * kChunk < nkb; ++c) {
             const int b = c & 1, cnt = min(kChunk, nkb - c * kChunk);
-            if (!mbar_wait_lane0(&scl_empty[b], (uint32_t)(((c >> 1) & 1) ^ 1), lane, status)) break;
+            if (!mbar_wait_warp(&scl_empty[b], (uint32_t)(((c >> 1) & 1) ^ 1), status)) break;
             for (int r = (warp - 2) * 32 + lane; r < MT; r += 64) {
                 const bool live = m0 + r < M;
                 const float *as_row = as + (int64_t)(live ? m0 + r : 0) * kb_all + kb0;
@@ -354,8 +348,8 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         bool ok = true;
         for (int i = 0; i < nkb; ++i) {
             const int b = i & 1, ch = i / kChunk;
-            ok = i % kChunk || f8_warp_wait(&scl_full[ch & 1], (uint32_t)((ch >> 1) & 1), status);
-            if (!ok || !(ok = f8_warp_wait(&acc_full[b], (uint32_t)((i >> 1) & 1), status))) break;
+            ok = i % kChunk || mbar_wait_warp(&scl_full[ch & 1], (uint32_t)((ch >> 1) & 1), status);
+            if (!ok || !(ok = mbar_wait_warp(&acc_full[b], (uint32_t)((i >> 1) & 1), status))) break;
             tc_fence_after();
             uint32_t d[COLS];
             f8_tmem_ld(tm + b * MT, d);
@@ -405,7 +399,7 @@ fp8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         if constexpr (Cfg::ASYNC) f8_cluster_arrive_relaxed();   // (the sums signal for themselves)
         else f8_cluster_arrive();
         bool here = true;   // the sums of every CTA of the cluster have arrived in this one
-        if constexpr (Cfg::ASYNC) here = f8_warp_wait(parts, 0, status);
+        if constexpr (Cfg::ASYNC) here = mbar_wait_warp(parts, 0, status);
         else f8_cluster_wait();
         if (here && cpr >= 4) f8_sum_parts<MT, 4, OUT_BF16>(sm, y, tid, m0 + crank * cpr, n0, M, N, split, cpr);
         else if (here) f8_sum_parts<MT, 2, OUT_BF16>(sm, y, tid, m0 + crank * cpr, n0, M, N, split, cpr);
@@ -557,7 +551,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
         if constexpr (Cfg::SPLIT_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 0) {
             for (; pit < total;) {
-                if (!f8_warp_wait(&empty[ps], (uint32_t)(((pit / STAGES) & 1) ^ 1), status)) break;
+                if (!mbar_wait_warp(&empty[ps], (uint32_t)(((pit / STAGES) & 1) ^ 1), status)) break;
                 load_stage();
             }
             // before the CTA may exit: the latest load armed on each stage has landed ..
@@ -567,7 +561,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             }
             // .. and the leader's commit of the MMAs that read it has arrived here: the loop's waits, STAGES blocks on
             for (int i = pit; pit == total && i < total + STAGES; ++i) {
-                if (!f8_warp_wait(&empty[ps], (uint32_t)(((i / STAGES) & 1) ^ 1), status)) break;
+                if (!mbar_wait_warp(&empty[ps], (uint32_t)(((i / STAGES) & 1) ^ 1), status)) break;
                 if (++ps == STAGES) ps = 0;
             }
             if (rank == 1) mbar_wait(drain, 0, status);   // (the leader's last commit arrives in both CTAs)
@@ -579,7 +573,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             bool ready = false;
             for (; it < total; ++it) {
                 if ((BUFS != 4 || !__all_sync(0xffffffffu, ready)) &&
-                    (!f8_warp_wait(&full[s], ph, status) || !f8_warp_wait(&acc_empty[b], bph, status)))
+                    (!mbar_wait_warp(&full[s], ph, status) || !mbar_wait_warp(&acc_empty[b], bph, status)))
                     break;
                 if constexpr (BUFS == 4) __syncwarp();
                 tc_fence_after();
@@ -612,7 +606,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             // before this CTA may exit: the promotion warps of both CTAs have given back each accumulator's last sums (the
             // loop's waits, BUFS blocks on)
             for (int i = 0; it == total && i < BUFS; ++i) {
-                if (!f8_warp_wait(&acc_empty[b], bph, status)) break;
+                if (!mbar_wait_warp(&acc_empty[b], bph, status)) break;
                 if (++b == BUFS) {
                     b = 0;
                     bph ^= 1;
@@ -665,7 +659,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
             int b = 0;
             uint32_t ph = 1;
             for (int it = 0; it < total; ++it) {
-                if (it >= BUFS && !f8_warp_wait(&acc_full[b], ph, status)) break;
+                if (it >= BUFS && !mbar_wait_warp(&acc_full[b], ph, status)) break;
                 fetch(it + kWFacAhead);
                 cp_async_wait<kWFacAhead>();
                 __syncwarp();
@@ -694,7 +688,7 @@ fp8_gemm_wide_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_con
 #pragma unroll
             for (int j = 0; j < 32; ++j) acc[j] = 0ull;
             for (int k = 0; k < num_k; ++k) {
-                if (!(ok = f8_warp_wait(&acc_full[b], bph, status))) break;
+                if (!(ok = mbar_wait_warp(&acc_full[b], bph, status))) break;
                 tc_fence_after();
                 // two loads of 32 columns in one set of registers (four of 16 in two sets, each under way while the one
                 // before was added, with scalar sums: 32768 x 2048 x 4096 282 us back to back, so 267)

@@ -271,7 +271,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 uint32_t ra[16], rb[32];
                 // the stage's operands (and scale tiles) have landed in this CTA; the tensor-memory
                 // slot is free then too (the producer refilled the stage after the MMAs released it)
-                if (!(ok = mbar_wait_lane0(&full[s], ph, lane, status))) break;
+                if (!(ok = mbar_wait_warp(&full[s], ph, status))) break;
                 if (sf_tma) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -314,7 +314,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         int j = 0;
         for (int t = pair; t < num_tiles && ok; t += npairs, ++j) {
             const int tile_m = t / tiles_n, tile_n = t % tiles_n;
-            if (!(ok = mbar_wait_lane0(acc_full, (uint32_t)(j & 1), lane, status))) break;
+            if (!(ok = mbar_wait_warp(acc_full, (uint32_t)(j & 1), status))) break;
             tc_fence_after();
             const int row = tile_m * 256 + (int)rank * 128 + quarter * 32 + lane;
 #pragma unroll 1

@@ -164,7 +164,7 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
                 const int s = it % kPoolStages;
                 const float ga = gate_at(d.a, d.gate_bf16, row * d.ldg + h), gb = gate_at(d.b, d.gate_bf16, row * d.ldg + h);
                 const float ge = d.A_log[h], gt = d.dt_bias[h];
-                if (it >= kPoolStages) ok = mbar_wait_lane0(&sm.empty[s], (uint32_t)(((it / kPoolStages) & 1) ^ 1), lane, d.status);
+                if (it >= kPoolStages) ok = mbar_wait_warp(&sm.empty[s], (uint32_t)(((it / kPoolStages) & 1) ^ 1), d.status);
                 if (!ok) break;
                 const int64_t vrow = ((int64_t)row * Hv + h) * kD, krow = ((int64_t)row * d.Hk + kh) * kD;
                 if (elect_one()) {
@@ -189,7 +189,7 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
                 }
                 __syncwarp();
             }
-            if (!mbar_wait_lane0(&sm.claimed, (uint32_t)((claims - 1) & 1), lane, d.status)) break;
+            if (!mbar_wait_warp(&sm.claimed, (uint32_t)((claims - 1) & 1), d.status)) break;
             unit = claimed_unit(&sm.claim);
             __syncwarp();
         }
@@ -217,14 +217,14 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
         for (int it = first, step = warp - kPoolWarps;; it += step, step = kPoolFinishers) {
             const bool run = it >= 0;
             const int s = run ? it % kPoolStages : 0, ob = run ? it % kPoolRows : 0;
-            if (run && !mbar_wait_lane0(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), lane, d.status)) break;
+            if (run && !mbar_wait_warp(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), d.status)) break;
             const int row = sm.meta[s].row, head = sm.meta[s].head;
             if (run && row < 0) break;
             uint4 zu = make_uint4(0u, 0u, 0u, 0u);
             if constexpr (TAIL) zu = *reinterpret_cast<const uint4 *>(&sm.z[s][col]);
             __syncwarp();
             if (run && lane == 0) mbar_arrive(&sm.empty[s]);
-            if (run && !mbar_wait_lane0(&sm.o_full[ob], (uint32_t)((it / kPoolRows) & 1), lane, d.status)) break;
+            if (run && !mbar_wait_warp(&sm.o_full[ob], (uint32_t)((it / kPoolRows) & 1), d.status)) break;
             const float4 oa = *reinterpret_cast<const float4 *>(&sm.o[ob][col]);
             const float4 oc = *reinterpret_cast<const float4 *>(&sm.o[ob][col + 4]);
             __syncwarp();
@@ -267,7 +267,7 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
     for (int it = first;; ++it) {
         const bool run = it >= 0;
         const int s = run ? it % kPoolStages : 0, ob = run ? it % kPoolRows : 0;
-        if (run && !mbar_wait_lane0(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), lane, d.status)) break;
+        if (run && !mbar_wait_warp(&sm.full[s], (uint32_t)((it / kPoolStages) & 1), d.status)) break;
         const PoolMeta m = sm.meta[s];
         if (run && m.row < 0) break;
 
@@ -312,7 +312,7 @@ gdn_decode128_pooled_kernel(const __grid_constant__ PooledDecodeArgs d) {
         for (int p = 0; p < 2; ++p) part[p] = pool_dot16(st[p], q2);
         const float ot = pool_sum2(part, l8) * qn;
         // the row that this buffer held has been finished
-        if (run && !mbar_wait_lane0(&sm.o_empty[ob], (uint32_t)(((it / kPoolRows) & 1) ^ 1), lane, d.status)) break;
+        if (run && !mbar_wait_warp(&sm.o_empty[ob], (uint32_t)(((it / kPoolRows) & 1) ^ 1), d.status)) break;
         if (run && (l8 & 3) == 0) sm.o[ob][rbase + 64 * (l8 >> 2)] = ot;
         __syncwarp();
         if (run && lane == 0) mbar_arrive(&sm.o_full[ob]);

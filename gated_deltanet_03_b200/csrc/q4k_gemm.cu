@@ -221,7 +221,7 @@ q4k_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const uint8_t *__rest
                 ds[h2] = d * (float)scale;
                 dm[h2] = dmin * (float)mn;
             }
-            if (!(ok = mbar_wait_lane0(&empty[s], (uint32_t)(((i / QK_STAGES) & 1) ^ 1), lane, status))) break;
+            if (!(ok = mbar_wait_warp(&empty[s], (uint32_t)(((i / QK_STAGES) & 1) ^ 1), status))) break;
             // values 0-31 of the stage: low nibbles (sub-block 2 g); 32-63: high nibbles (2 g + 1).
             // Two quants at a time as bf16 pairs: a byte permute puts the nibbles of two adjacent
             // bytes into the two 16-bit halves, OR-ing in the exponent of 128 makes them the bf16
@@ -252,7 +252,7 @@ q4k_gemm_kernel(const __grid_constant__ CUtensorMap map_a, const uint8_t *__rest
             if (lane == 0) mbar_arrive(&b_full[s]);
         }
         // epilogue: this warp's lane quarter of the 128 x 128 accumulator, one output row per thread
-        if (ok) ok = mbar_wait_lane0(acc_full, 0, lane, status);
+        if (ok) ok = mbar_wait_warp(acc_full, 0, status);
         if (ok && BN == 128 && split > 1) {
             // the partial tile into this CTA's shared memory (the stage ring is idle: every load
             // was consumed by an MMA that has completed), row = tensor-memory lane
