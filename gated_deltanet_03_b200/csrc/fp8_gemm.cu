@@ -146,8 +146,8 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[N]) {
 __device__ __forceinline__ void f8_tmem_ld(uint32_t at, uint32_t (&d)[16]) { tmem_ld16(at, d); }
 __device__ __forceinline__ void f8_tmem_ld(uint32_t at, uint32_t (&d)[32]) { tmem_ld32(at, d); }
 
-// mbar_wait_warp on two barriers, the first look at both in one instruction (even lanes at one, odd lanes at the other; __syncwarp
-// makes what each half has seen complete so for the other, which the vote does not).
+// mbar_wait_warp on two barriers, the first look at both in one instruction (even lanes at one, odd lanes at the other;
+// __syncwarp makes what each half has seen complete so for the other, which the vote does not).
 __device__ __forceinline__ bool f8_warp_wait2(uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1, int *status) {
     const bool odd = threadIdx.x & 1;
     if (__all_sync(0xffffffffu, mbar_try_wait(odd ? b1 : b0, odd ? p1 : p0))) {

@@ -21,8 +21,8 @@
 // without a wait or a store: it brings the loop's code into the SM's instruction cache while the first state is on
 // its way. Without it a CTA's first item took 12,700 cycles from its state's arrival to its codes, later ones a
 // third of that, which is most of a small batch's time.
-// 250 live rows x 32 heads take 161.3 us plain and 162.0 with the tail (the bytes at the measured copy rate: 161), 3 live
-// rows x 16 heads 4.9 and 5.1.
+// 250 live rows x 32 heads take 161.3 us plain and 161.8 with the tail (the bytes at the measured copy rate: 161), 3 live
+// rows x 16 heads 4.3 and 4.6.
 // A row with a negative slot is passed over (its outputs stay as they are); so is a row whose slot is not
 // below num_slots or is named by an earlier row, and the status word then reads GDN_ERR_INVALID_ARG.
 // Every wait is bounded; an expired one records GDN_ERR_TIMEOUT and the warp ends.
